@@ -18,14 +18,15 @@ __all__ = [
     "gdn2_chunk_fwd_varlen", "gdn2_chunk_fwd_varlen_workspace",
     "gdn_chunk_fwd_workspace", "gdn2_chunk_fwd_workspace", "gdn_prologue", "gdn_gated_rmsnorm",
     "gdn2_chunk_bwd", "gdn2_chunk_bwd_workspace", "gdn2_chunk_fwd_noalloc", "gdn2_chunk_fwd_noalloc_max_bytes",
+    "gdn_add_rmsnorm", "gdn_add_rmsnorm_bwd", "gdn_add_rmsnorm_bwd_workspace", "gdn_quantize_rows",
     "clock_probe",
-    "GDN_F32", "GDN_BF16", "BT",
+    "GDN_F32", "GDN_BF16", "GDN_F8E4M3", "BT",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libgdn.so")
 
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_F8E4M3 = 0, 1, 2
 BT = 64
 _lib = None
 
@@ -85,6 +86,15 @@ def load():
     lib.gdn_clock_probe.argtypes = [_vp, _i, _i, _vp]
     lib.gdn_gated_rmsnorm.restype = _i
     lib.gdn_gated_rmsnorm.argtypes = [_vp] * 4 + [ctypes.c_longlong, _i, _f, _vp]
+    _ll = ctypes.c_longlong
+    lib.gdn_add_rmsnorm.restype = _i
+    lib.gdn_add_rmsnorm.argtypes = [_vp] * 7 + [_ll, _i, _i, _i, _i, _f, _vp]
+    lib.gdn_add_rmsnorm_bwd_workspace.restype = _sz
+    lib.gdn_add_rmsnorm_bwd_workspace.argtypes = [_ll, _i]
+    lib.gdn_add_rmsnorm_bwd.restype = _i
+    lib.gdn_add_rmsnorm_bwd.argtypes = [_vp] * 7 + [_ll, _i, _i, _i, _vp, _sz, _vp]
+    lib.gdn_quantize_rows.restype = _i
+    lib.gdn_quantize_rows.argtypes = [_vp] * 3 + [_ll, _i, _i, _vp]
     _lib = lib
     return lib
 
@@ -579,6 +589,122 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-5, out=None):
     _check(load().gdn_gated_rmsnorm(_ptr(o), _ptr(z), _ptr(weight), _ptr(y), rows, Dv, float(eps), _stream(dev)),
            "gdn_gated_rmsnorm")
     return y
+
+
+def _codes():
+    torch = _torch()
+    return {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_F8E4M3}
+
+
+def _code(t, name):
+    code = _codes().get(t)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float8_e4m3fn, got {t}")
+    return code
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(fn, what, dev, args):
+    """Calls fn(*args, stream) with dev as the current device, on its current stream."""
+    torch = _torch()
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on the GPU, got {dev}")
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if code:
+        _check(code, what)
+
+
+def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-5, out_dtype=None, return_rstd=False, out=None,
+                    residual_out=None):
+    """Residual addition and RMS norm over the last axis: u = x + residual, y = u / sqrt(mean(u^2) + eps) * weight.
+    x [..., D] bf16 or fp32, weight [D] fp32, residual [..., D] in the type of x or fp32, or None.  out_dtype: the
+    type of x (default) or torch.float8_e4m3fn, with one fp32 scale per row.  residual_out may be residual itself (in
+    place).  Returns (y, r, rstd, y_scale): r = u in the type of residual (None without one), rstd [rows] when
+    return_rstd, y_scale [rows] for 8-bit y, None otherwise."""
+    torch = _torch()
+    shape, dev, f32 = tuple(x.shape), x.device, torch.float32
+    if not shape:
+        raise ValueError("x must have at least one axis")
+    D = shape[-1]
+    rows = x.numel() // D if D else 0
+    _need(x, "x", shape, x.dtype, dev)
+    _need(weight, "weight", (D,), f32, dev)
+    rdt = x.dtype
+    r = None
+    if residual is not None:
+        rdt = residual.dtype
+        _need(residual, "residual", shape, rdt, dev)
+        r = residual_out if residual_out is not None else torch.empty(shape, dtype=rdt, device=dev)
+        _need(r, "residual_out", shape, rdt, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    odt = x.dtype if out_dtype is None else out_dtype
+    y = out if out is not None else torch.empty(shape, dtype=odt, device=dev)
+    _need(y, "out", shape, odt, dev)
+    rstd = torch.empty(shape[:-1], dtype=f32, device=dev) if return_rstd else None
+    y_scale = torch.empty(shape[:-1], dtype=f32, device=dev) if odt == torch.float8_e4m3fn else None
+    _on_device(load().gdn_add_rmsnorm, "gdn_add_rmsnorm", dev,
+               (_addr(x), _addr(residual), _addr(weight), _addr(y), _addr(r), _addr(rstd), _addr(y_scale), rows, D,
+                _code(x.dtype, "x"), _code(rdt, "residual"), _code(odt, "out_dtype"), float(eps)))
+    return y, r, rstd, y_scale
+
+
+def gdn_add_rmsnorm_bwd_workspace(rows, D):
+    return int(load().gdn_add_rmsnorm_bwd_workspace(rows, D))
+
+
+def gdn_add_rmsnorm_bwd(dy, r, weight, rstd, dr=None, need_dweight=True, workspace=None):
+    """Gradients of gdn_add_rmsnorm.  dy [..., D] bf16 or fp32; r [..., D]: what the forward returned (x when it had
+    no residual); rstd [...] fp32; dr [..., D]: gradient that reaches r from elsewhere, or None.  Returns (dx in the
+    type of r: the gradient of x and of residual alike, dweight [D] fp32 or None)."""
+    torch = _torch()
+    shape, dev, f32 = tuple(dy.shape), dy.device, torch.float32
+    if not shape:
+        raise ValueError("dy must have at least one axis")
+    D = shape[-1]
+    rows = dy.numel() // D if D else 0
+    _need(dy, "dy", shape, dy.dtype, dev)
+    _need(r, "r", shape, r.dtype, dev)
+    _need(weight, "weight", (D,), f32, dev)
+    _need(rstd, "rstd", shape[:-1], f32, dev)
+    if dr is not None:
+        _need(dr, "dr", shape, r.dtype, dev)
+    dx = torch.empty(shape, dtype=r.dtype, device=dev)
+    dw = ws = None
+    nbytes = 0
+    lib = load()
+    if need_dweight:
+        dw = torch.empty((D,), dtype=f32, device=dev)
+        need = lib.gdn_add_rmsnorm_bwd_workspace(rows, D)
+        ws = workspace if workspace is not None else _workspace(need, dev)[1]
+        nbytes = ws.numel() * ws.element_size()
+    _on_device(lib.gdn_add_rmsnorm_bwd, "gdn_add_rmsnorm_bwd", dev,
+               (_addr(dy), _addr(r), _addr(weight), _addr(rstd), _addr(dr), _addr(dx), _addr(dw), rows, D,
+                _code(dy.dtype, "dy"), _code(r.dtype, "r"), _addr(ws), nbytes))
+    return dx, dw
+
+
+def gdn_quantize_rows(x):
+    """Rows of x [..., D] (bf16 or fp32) in 8 bits: (q float8_e4m3fn [..., D], scale [...] fp32) with
+    scale = max|x| / 448 (1 for a row of zeros) and q = x / scale."""
+    torch = _torch()
+    shape, dev = tuple(x.shape), x.device
+    if not shape:
+        raise ValueError("x must have at least one axis")
+    D = shape[-1]
+    _need(x, "x", shape, x.dtype, dev)
+    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    _on_device(load().gdn_quantize_rows, "gdn_quantize_rows", dev,
+               (_addr(x), _addr(q), _addr(scale), x.numel() // D if D else 0, D, _code(x.dtype, "x")))
+    return q, scale
 
 
 def clock_probe(nblocks=256, spin_us=2000, device="cuda"):

@@ -592,4 +592,79 @@ gdn_status gdn_gated_rmsnorm(const float *o, const void *z, const float *weight,
     return from_hip(gdn::launch_gated_rmsnorm(o, z, weight, y, (long)rows, Dv, eps, (hipStream_t)stream));
 }
 
+// Element size of the types the norm and linear entry points take.
+static size_t esize3(gdn_dtype dt) { return dt == GDN_F32 ? 4 : dt == GDN_BF16 ? 2 : 1; }
+
+static bool norm_types_ok(gdn_dtype dtype, gdn_dtype rdtype) {
+    return dtype_ok(dtype) && dtype_ok(rdtype) && (rdtype == GDN_F32 || dtype == GDN_BF16);
+}
+
+// rows * D elements of 4 bytes must stay within an address range
+static bool rows_ok(long long rows, int D) { return rows >= 1 && D >= 1 && rows < (1LL << 40); }
+
+gdn_status gdn_add_rmsnorm(const void *x, const void *residual, const float *weight, void *y, void *r, float *rstd,
+                           float *y_scale, long long rows, int D, gdn_dtype dtype, gdn_dtype rdtype,
+                           gdn_dtype out_dtype, float eps, void *stream) {
+    if (!x || !weight || !y || !rows_ok(rows, D) || !(eps > 0.f)) return GDN_ERR_INVALID_ARG;
+    if (!norm_types_ok(dtype, rdtype) || D > gdn::kMaxNormCols) return GDN_ERR_UNSUPPORTED;
+    const bool f8 = out_dtype == GDN_F8E4M3;
+    if (!f8 && out_dtype != dtype) return GDN_ERR_UNSUPPORTED;
+    if (f8 != (y_scale != nullptr) || (r && !residual)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(r, 16) || !aligned(y, f8 ? 8 : 16) || !aligned(weight, 4) ||
+        !aligned(rstd, 4) || !aligned(y_scale, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t n = (size_t)rows * D;
+    const Range ins[] = {{x, n * esize3(dtype)}, {weight, (size_t)D * 4}, {residual, n * esize3(rdtype)}};
+    const Range outs[] = {{y, n * esize3(out_dtype)}, {rstd, (size_t)rows * 4}, {y_scale, (size_t)rows * 4},
+                          {r, n * esize3(rdtype)}};
+    for (int a = 0; a < 4; ++a) {
+        for (int c = 0; c < 3; ++c)
+            if (overlap(outs[a], ins[c]) && !(a == 3 && c == 2 && r == residual)) return GDN_ERR_INVALID_ARG;
+        for (int c = a + 1; c < 4; ++c)
+            if (overlap(outs[a], outs[c])) return GDN_ERR_INVALID_ARG;
+    }
+    return from_hip(gdn::launch_add_rmsnorm(x, residual, weight, y, r, rstd, y_scale, (long)rows, D,
+                                            dtype == GDN_BF16, rdtype == GDN_BF16, f8, eps, (hipStream_t)stream));
+}
+
+size_t gdn_add_rmsnorm_bwd_workspace(long long rows, int D) {
+    if (!rows_ok(rows, D) || D > gdn::kMaxNormCols) return 0;
+    return align_up((size_t)gdn::norm_bwd_blocks((long)rows, D) * D * sizeof(float));
+}
+
+gdn_status gdn_add_rmsnorm_bwd(const void *dy, const void *r, const float *weight, const float *rstd, const void *dr,
+                               void *dx, float *dweight, long long rows, int D, gdn_dtype dtype, gdn_dtype rdtype,
+                               void *ws, size_t ws_bytes, void *stream) {
+    if (!dy || !r || !weight || !rstd || !dx || !rows_ok(rows, D)) return GDN_ERR_INVALID_ARG;
+    if (!norm_types_ok(dtype, rdtype) || D > gdn::kMaxNormCols) return GDN_ERR_UNSUPPORTED;
+    if (!aligned(dy, 16) || !aligned(r, 16) || !aligned(dr, 16) || !aligned(dx, 16) || !aligned(weight, 4) ||
+        !aligned(rstd, 4) || !aligned(dweight, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t need = dweight ? gdn_add_rmsnorm_bwd_workspace(rows, D) : 0;
+    if (dweight && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    const size_t n = (size_t)rows * D;
+    const Range ins[] = {{dy, n * esize3(dtype)}, {r, n * esize3(rdtype)}, {weight, (size_t)D * 4},
+                         {rstd, (size_t)rows * 4}, {dr, n * esize3(rdtype)}};
+    const Range outs[] = {{dx, n * esize3(rdtype)}, {dweight, (size_t)D * 4}, {dweight ? ws : nullptr, need}};
+    for (int a = 0; a < 3; ++a) {
+        for (Range in : ins)
+            if (overlap(outs[a], in)) return GDN_ERR_INVALID_ARG;
+        for (int c = a + 1; c < 3; ++c)
+            if (overlap(outs[a], outs[c])) return GDN_ERR_INVALID_ARG;
+    }
+    return from_hip(gdn::launch_add_rmsnorm_bwd(dy, r, weight, rstd, dr, dx, dweight, (float *)ws, (long)rows, D,
+                                                dtype == GDN_BF16, rdtype == GDN_BF16, (hipStream_t)stream));
+}
+
+gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long rows, int D, gdn_dtype dtype,
+                             void *stream) {
+    if (!x || !q || !scale || !rows_ok(rows, D)) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || D > gdn::kMaxNormCols) return GDN_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(q, 8) || !aligned(scale, 4)) return GDN_ERR_INVALID_ARG;
+    const size_t n = (size_t)rows * D;
+    const Range rx{x, n * esize3(dtype)}, rq{q, n}, rs{scale, (size_t)rows * 4};
+    if (overlap(rq, rx) || overlap(rs, rx) || overlap(rq, rs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_quantize_rows(x, q, scale, (long)rows, D, dtype == GDN_BF16, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -130,4 +130,22 @@ hipError_t launch_prologue(const void *xq, const void *xk, const void *xv, const
 hipError_t launch_gated_rmsnorm(const float *o, const void *z, const float *w, void *y, long rows, int Dv, float eps,
                                 hipStream_t st);
 
+// The block's entry (gdn_norm.hip): u = x + res (res nullable), rout = u,
+// y = u s w with s = (mean(u^2) + eps)^-1/2 into rstd; y in the type of x, or
+// (f8) e4m3 with one scale per row.  Types (x, res): (bf16, bf16),
+// (bf16, fp32), (fp32, fp32).  D <= kMaxNormCols.
+constexpr int kMaxNormCols = 32768;
+hipError_t launch_add_rmsnorm(const void *x, const void *res, const float *w, void *y, void *rout, float *rstd,
+                              float *yscale, long rows, int D, bool x_bf16, bool r_bf16, bool f8, float eps,
+                              hipStream_t st);
+hipError_t launch_quantize_rows(const void *x, void *q, float *scale, long rows, int D, bool bf16, hipStream_t st);
+// Backward; part holds norm_bwd_blocks(rows, D) rows of D partial column sums
+// (used when dw is wanted).
+int norm_bwd_blocks(long rows, int D);
+hipError_t launch_add_rmsnorm_bwd(const void *dy, const void *r, const float *w, const float *rstd, const void *dr,
+                                  void *dx, float *dw, float *part, long rows, int D, bool dy_bf16, bool r_bf16,
+                                  hipStream_t st);
+// out[c] = sum of n rows of part [n, D], in a fixed order.
+hipError_t launch_colsum(const float *part, float *out, int n, int D, hipStream_t st);
+
 }  // namespace gdn

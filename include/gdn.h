@@ -71,7 +71,9 @@ typedef enum {
     GDN_ERR_HIP = 4           /* a HIP launch failed */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* GDN_F8E4M3 (8 bits: sign, 4 exponent, 3 mantissa bits, largest finite value
+ * 448, no infinities) is taken by the entry points that name it only. */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F8E4M3 = 2 } gdn_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *gdn_status_string(gdn_status s);
@@ -364,6 +366,67 @@ gdn_status gdn_prologue(const void *xq, const void *xk, const void *xv, const fl
  */
 gdn_status gdn_gated_rmsnorm(const float *o, const void *z, const float *weight, void *y,
                              long long rows, int Dv, float eps, void *stream);
+
+/*
+ * gdn_add_rmsnorm -- the block's entry, before the layer's projections: the
+ * residual addition and the RMS norm in one pass, with an output in the
+ * input's type or in 8 bits.  Per row of D:
+ *   u = x + residual (u = x without one);  r = u
+ *   s = (mean(u^2) + eps)^-1/2;  y = u * s * weight
+ *   8-bit output: y_scale = max|u s weight| / 448 (1 for a row of zeros),
+ *   y = e4m3(u s weight / y_scale), rounded to nearest even
+ * All of it in fp32 with one rounding per output; s is taken of the fp32 sum,
+ * before r is rounded to its type.
+ *   x        [rows, D] dtype (GDN_BF16 or GDN_F32)
+ *   residual [rows, D] rdtype, nullable.  rdtype: GDN_F32, or GDN_BF16 with bf16 x
+ *   weight   [D] fp32
+ *   y        [rows, D] out_dtype: dtype or GDN_F8E4M3
+ *   r        [rows, D] rdtype, nullable, only with a residual: the residual
+ *            stream after the addition; may be residual itself (in place)
+ *   rstd     [rows] fp32, nullable: s, for gdn_add_rmsnorm_bwd
+ *   y_scale  [rows] fp32: required with 8-bit output, null otherwise
+ * 1 <= D <= 32768, any value.  x, residual, y and r are 16-byte aligned
+ * (8-bit y: 8-byte); rows need not be.  A row that holds an infinity or a NaN
+ * gives NaN codes and scale in 8 bits.  u^2 must not overflow fp32.
+ * Errors: GDN_ERR_INVALID_ARG (null required pointers, a y_scale or r that
+ * does not belong, rows < 1, D < 1, eps <= 0, misalignment, an output that
+ * overlaps an input or another output), GDN_ERR_UNSUPPORTED (D > 32768 or
+ * types not listed), GDN_ERR_HIP.  Asynchronous on `stream`; no workspace.
+ */
+gdn_status gdn_add_rmsnorm(const void *x, const void *residual, const float *weight, void *y, void *r, float *rstd,
+                           float *y_scale, long long rows, int D, gdn_dtype dtype, gdn_dtype rdtype,
+                           gdn_dtype out_dtype, float eps, void *stream);
+
+/*
+ * gdn_add_rmsnorm_bwd -- gradients of gdn_add_rmsnorm (not of the rounding to
+ * 8 bits) for L = sum(dy . y) + sum(dr . r):
+ *   xhat = r * rstd;  dx = rstd (w dy - xhat mean(w dy xhat)) + dr
+ *   dweight = sum over rows of dy xhat
+ * dx is the gradient of x and of residual alike.
+ *   dy [rows, D] dtype;  r [rows, D] rdtype (x when there was no residual);
+ *   weight [D], rstd [rows] fp32;  dr [rows, D] rdtype, nullable;
+ *   dx [rows, D] rdtype;  dweight [D] fp32, nullable
+ *   ws  gdn_add_rmsnorm_bwd_workspace() bytes, 256-byte aligned (may be NULL
+ *       without dweight)
+ * Types, sizes, alignment and errors as gdn_add_rmsnorm, plus
+ * GDN_ERR_WORKSPACE.  The sums over rows are formed in a fixed order.
+ */
+size_t gdn_add_rmsnorm_bwd_workspace(long long rows, int D);
+
+gdn_status gdn_add_rmsnorm_bwd(const void *dy, const void *r, const float *weight, const float *rstd, const void *dr,
+                               void *dx, float *dweight, long long rows, int D, gdn_dtype dtype, gdn_dtype rdtype,
+                               void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * gdn_quantize_rows -- rows in 8 bits with one scale each, for the weights
+ * and activations of gdn_linear that no norm quantises:
+ *   scale = max|x| / 448 (1 for a row of zeros);  q = e4m3(x / scale)
+ *   x [rows, D] dtype (GDN_BF16 or GDN_F32), 16-byte aligned;
+ *   q [rows, D] e4m3, 8-byte aligned;  scale [rows] fp32
+ * 1 <= D <= 32768.  Errors as gdn_add_rmsnorm.  Asynchronous; no workspace.
+ */
+gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long rows, int D, gdn_dtype dtype,
+                             void *stream);
 
 /*
  * gdn_clock_probe -- measurement aid, not part of the operation: enqueues
