@@ -19,6 +19,7 @@ __all__ = [
     "gdn_chunk_fwd_workspace", "gdn2_chunk_fwd_workspace", "gdn_prologue", "gdn_gated_rmsnorm",
     "gdn2_chunk_bwd", "gdn2_chunk_bwd_workspace", "gdn2_chunk_fwd_noalloc", "gdn2_chunk_fwd_noalloc_max_bytes",
     "gdn_add_rmsnorm", "gdn_add_rmsnorm_bwd", "gdn_add_rmsnorm_bwd_workspace", "gdn_quantize_rows",
+    "gdn_linear", "gdn_linear_workspace", "gdn_linear_bwd", "gdn_linear_bwd_workspace",
     "clock_probe",
     "GDN_F32", "GDN_BF16", "GDN_F8E4M3", "BT",
 ]
@@ -95,6 +96,14 @@ def load():
     lib.gdn_add_rmsnorm_bwd.argtypes = [_vp] * 7 + [_ll, _i, _i, _i, _vp, _sz, _vp]
     lib.gdn_quantize_rows.restype = _i
     lib.gdn_quantize_rows.argtypes = [_vp] * 3 + [_ll, _i, _i, _vp]
+    lib.gdn_linear_workspace.restype = _sz
+    lib.gdn_linear_workspace.argtypes = [_i] * 4
+    lib.gdn_linear.restype = _i
+    lib.gdn_linear.argtypes = [_vp] * 8 + [_i] * 6 + [_vp, _sz, _vp]
+    lib.gdn_linear_bwd_workspace.restype = _sz
+    lib.gdn_linear_bwd_workspace.argtypes = [_i] * 9
+    lib.gdn_linear_bwd.restype = _i
+    lib.gdn_linear_bwd.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
     _lib = lib
     return lib
 
@@ -705,6 +714,111 @@ def gdn_quantize_rows(x):
     _on_device(load().gdn_quantize_rows, "gdn_quantize_rows", dev,
                (_addr(x), _addr(q), _addr(scale), x.numel() // D if D else 0, D, _code(x.dtype, "x")))
     return q, scale
+
+
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _act_code(act):
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return code
+
+
+def gdn_linear_workspace(M, N, K, dtype_code):
+    return int(load().gdn_linear_workspace(M, N, K, dtype_code))
+
+
+def gdn_linear(x, weight, bias=None, residual=None, act="none", x_scale=None, w_scale=None, out_dtype=None,
+               return_preact=False, workspace=None, out=None):
+    """Matrix product with its epilogue: z = (x weight^T) x_scale w_scale + bias, y = act(z) + residual.
+    x [..., K], weight [N, K], both bf16, or both float8_e4m3fn with x_scale [...] and w_scale [N] fp32; bias [N] fp32;
+    residual [..., N] in out_dtype (bf16, the default, or fp32; out may be residual itself); act: none, relu, silu or
+    gelu.  K is a multiple of 8 (16 in 8 bits).  Returns (y [..., N], z bf16 or None): z, the activation's argument,
+    with return_preact."""
+    torch = _torch()
+    dev, dt = x.device, x.dtype
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError("x must be [..., K] and weight [N, K]")
+    K, N = x.shape[-1], weight.shape[0]
+    lead = tuple(x.shape[:-1])
+    _need(x, "x", lead + (K,), dt, dev)
+    _need(weight, "weight", (N, K), dt, dev)
+    M = x.numel() // K if K else 0
+    f32 = torch.float32
+    if dt == torch.float8_e4m3fn:
+        _need(x_scale, "x_scale", lead, f32, dev)
+        _need(w_scale, "w_scale", (N,), f32, dev)
+    elif x_scale is not None or w_scale is not None:
+        raise ValueError("x_scale and w_scale belong to float8_e4m3fn operands")
+    if bias is not None:
+        _need(bias, "bias", (N,), f32, dev)
+    odt = torch.bfloat16 if out_dtype is None else out_dtype
+    shape = lead + (N,)
+    if residual is not None:
+        _need(residual, "residual", shape, odt, dev)
+    y = out if out is not None else torch.empty(shape, dtype=odt, device=dev)
+    _need(y, "out", shape, odt, dev)
+    z = torch.empty(shape, dtype=torch.bfloat16, device=dev) if return_preact else None
+    lib = load()
+    code, ocode = _code(dt, "x"), _code(odt, "out_dtype")
+    ws, nbytes = workspace, 0
+    if ws is None:
+        need = lib.gdn_linear_workspace(M, N, K, code)
+        if need:
+            ws = _workspace(need, dev)[1]
+    if ws is not None:
+        nbytes = ws.numel() * ws.element_size()
+    _on_device(lib.gdn_linear, "gdn_linear", dev,
+               (_addr(x), _addr(weight), _addr(x_scale), _addr(w_scale), _addr(bias), _addr(residual), _addr(y),
+                _addr(z), M, N, K, code, ocode, _act_code(act), _addr(ws), nbytes))
+    return y, z
+
+
+def gdn_linear_bwd_workspace(M, N, K, dy_code, grad_code, act, need_dx=True, need_dw=True, need_dbias=False):
+    return int(load().gdn_linear_bwd_workspace(M, N, K, dy_code, grad_code, _act_code(act), int(need_dx),
+                                               int(need_dw), int(need_dbias)))
+
+
+def gdn_linear_bwd(dy, x, weight, z=None, act="none", bias=False, grad_dtype=None, need_dx=True, need_dw=True,
+                   workspace=None):
+    """Gradients of gdn_linear with bf16 x [..., K] and weight [N, K]: dz = dy act'(z), dx = dz weight, dw = dz^T x,
+    dbias = dz summed over rows.  dy [..., N] bf16 or fp32; z [..., N] bf16, what the forward returned with
+    return_preact (required with an activation).  grad_dtype of dx and dw: bf16 (default; dz is rounded to bf16 for the
+    products) or fp32 (dz is not rounded).  Returns (dx, dw, dbias fp32), None for what is not asked for; the gradient
+    of residual is dy."""
+    torch = _torch()
+    dev, bf = dy.device, torch.bfloat16
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError("x must be [..., K] and weight [N, K]")
+    K, N = x.shape[-1], weight.shape[0]
+    lead = tuple(x.shape[:-1])
+    _need(x, "x", lead + (K,), bf, dev)
+    _need(weight, "weight", (N, K), bf, dev)
+    _need(dy, "dy", lead + (N,), dy.dtype, dev)
+    if z is not None and act != "none":
+        _need(z, "z", lead + (N,), bf, dev)
+    elif act != "none":
+        raise ValueError(f"act {act!r} needs z")
+    M = x.numel() // K if K else 0
+    gdt = bf if grad_dtype is None else grad_dtype
+    dx = torch.empty(lead + (K,), dtype=gdt, device=dev) if need_dx else None
+    dw = torch.empty((N, K), dtype=gdt, device=dev) if need_dw else None
+    db = torch.empty((N,), dtype=torch.float32, device=dev) if bias else None
+    lib = load()
+    a, dyc, gc = _act_code(act), _code(dy.dtype, "dy"), _code(gdt, "grad_dtype")
+    ws, nbytes = workspace, 0
+    if ws is None:
+        need = lib.gdn_linear_bwd_workspace(M, N, K, dyc, gc, a, int(need_dx), int(need_dw), int(bool(bias)))
+        if need:
+            ws = _workspace(need, dev)[1]
+    if ws is not None:
+        nbytes = ws.numel() * ws.element_size()
+    _on_device(lib.gdn_linear_bwd, "gdn_linear_bwd", dev,
+               (_addr(dy), _addr(x), _addr(weight), _addr(z) if a else None, _addr(dx), _addr(dw), _addr(db), M, N, K,
+                dyc, gc, a, _addr(ws), nbytes))
+    return dx, dw, db
 
 
 def clock_probe(nblocks=256, spin_us=2000, device="cuda"):

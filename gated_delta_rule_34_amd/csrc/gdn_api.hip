@@ -28,6 +28,18 @@ bool overlap(Range a, Range b) {
     return a0 < b0 + b.n && b0 < a0 + a.n;
 }
 
+// No output may overlap an input, another output or the workspace.
+template <int NI, int NO>
+static bool disjoint(const Range (&ins)[NI], const Range (&outs)[NO]) {
+    for (int a = 0; a < NO; ++a) {
+        for (Range in : ins)
+            if (overlap(outs[a], in)) return false;
+        for (int c = a + 1; c < NO; ++c)
+            if (overlap(outs[a], outs[c])) return false;
+    }
+    return true;
+}
+
 // Workspace of the chunked forward: G2 [B,H,NT,64] fp32, then (T - I)
 // [B,H,NT,64,64] fp32, each section 256-byte aligned.
 struct ChunkWs {
@@ -665,6 +677,83 @@ gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long row
     const Range rx{x, n * esize3(dtype)}, rq{q, n}, rs{scale, (size_t)rows * 4};
     if (overlap(rq, rx) || overlap(rs, rx) || overlap(rq, rs)) return GDN_ERR_INVALID_ARG;
     return from_hip(gdn::launch_quantize_rows(x, q, scale, (long)rows, D, dtype == GDN_BF16, (hipStream_t)stream));
+}
+
+// Sizes of a product the kernels index: 32-bit offsets within a tile of 256
+// rows, a grid of fewer than 2^32 threads.
+static bool mm_sizes_ok(int M, int N, int K) {
+    auto tiles = [](long long a, long long b) { return ((a + 255) / 256) * ((b + 255) / 256) < (1LL << 22); };
+    return N <= (1 << 22) && K <= (1 << 22) && tiles(M, N) && tiles(M, K) && tiles(N, K);
+}
+
+static bool act_ok(gdn_act a) { return a >= GDN_ACT_NONE && a <= GDN_ACT_GELU; }
+
+static gdn_status linear_check(int M, int N, int K, gdn_dtype dtype) {
+    if (M < 1 || N < 1 || K < 1) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_F8E4M3) return GDN_ERR_UNSUPPORTED;
+    if (K % (dtype == GDN_BF16 ? 8 : 16) || !mm_sizes_ok(M, N, K)) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+size_t gdn_linear_workspace(int M, int N, int K, gdn_dtype dtype) {
+    if (linear_check(M, N, K, dtype) != GDN_OK) return 0;
+    return align_up(gdn::linear_ws_bytes(M, N, K, dtype == GDN_F8E4M3));
+}
+
+gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const float *w_scale, const float *bias,
+                      const void *residual, void *y, void *z, int M, int N, int K, gdn_dtype dtype,
+                      gdn_dtype out_dtype, gdn_act act, void *ws, size_t ws_bytes, void *stream) {
+    if (!x || !w || !y) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = linear_check(M, N, K, dtype);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(out_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
+    const bool f8 = dtype == GDN_F8E4M3;
+    if (f8 != (x_scale != nullptr) || f8 != (w_scale != nullptr)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(residual, 16) || !aligned(y, 16) || !aligned(z, 16) ||
+        !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_linear_workspace(M, N, K, dtype);
+    if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    const size_t mn = (size_t)M * N;
+    const Range ins[] = {{x, (size_t)M * K * esize3(dtype)}, {w, (size_t)N * K * esize3(dtype)},
+                         {x_scale, (size_t)M * 4}, {w_scale, (size_t)N * 4}, {bias, (size_t)N * 4},
+                         {residual == y ? nullptr : residual, mn * esize3(out_dtype)}};
+    const Range outs[] = {{y, mn * esize3(out_dtype)}, {z, mn * 2}, {need ? ws : nullptr, need}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_linear(x, w, x_scale, w_scale, bias, residual, y, z, M, N, K, f8, out_dtype == GDN_F32,
+                                       (int)act, (float *)ws, (hipStream_t)stream));
+}
+
+size_t gdn_linear_bwd_workspace(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
+                                int need_dx, int need_dw, int need_dbias) {
+    if (linear_check(M, N, K, GDN_BF16) != GDN_OK || !dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act))
+        return 0;
+    return gdn::linear_bwd_plan(M, N, K, dy_dtype == GDN_F32, grad_dtype == GDN_F32, (int)act, need_dx != 0,
+                                need_dw != 0, need_dbias != 0)
+        .total;
+}
+
+gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,
+                          float *dbias, int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
+                          void *ws, size_t ws_bytes, void *stream) {
+    if (!dy || !x || !w || (!dx && !dw && !dbias)) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = linear_check(M, N, K, GDN_BF16);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
+    if ((act != GDN_ACT_NONE) != (z != nullptr)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 16) || !aligned(dx, 16) ||
+        !aligned(dw, 16) || !aligned(dbias, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_linear_bwd_workspace(M, N, K, dy_dtype, grad_dtype, act, dx != nullptr, dw != nullptr,
+                                                 dbias != nullptr);
+    if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    const size_t mn = (size_t)M * N, mk = (size_t)M * K, nk = (size_t)N * K;
+    const Range ins[] = {{dy, mn * esize3(dy_dtype)}, {x, mk * 2}, {w, nk * 2}, {z, mn * 2}};
+    const Range outs[] = {{dx, mk * esize3(grad_dtype)}, {dw, nk * esize3(grad_dtype)}, {dbias, (size_t)N * 4},
+                          {need ? ws : nullptr, need}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_linear_bwd(dy, x, w, z, dx, dw, dbias, M, N, K, dy_dtype == GDN_F32,
+                                           grad_dtype == GDN_F32, (int)act, (char *)ws, (hipStream_t)stream));
 }
 
 }  // extern "C"

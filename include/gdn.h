@@ -428,6 +428,67 @@ gdn_status gdn_add_rmsnorm_bwd(const void *dy, const void *r, const float *weigh
 gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long rows, int D, gdn_dtype dtype,
                              void *stream);
 
+/* Activation of gdn_linear: none, max(z, 0), z sigmoid(z), z Phi(z) with the
+ * normal distribution function Phi. */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_RELU = 1, GDN_ACT_SILU = 2, GDN_ACT_GELU = 3 } gdn_act;
+
+/*
+ * gdn_linear -- the layer's projections (into q, k, v, z and the gates, out of
+ * the gated norm, and the feed-forward products around it), with everything
+ * that follows the product in its epilogue ("GatedDeltaNet walkthrough", the
+ * data-flow overview):
+ *   z = (x w^T) x_scale w_scale + bias;   y = act(z) + residual
+ *   x [M, K], w [N, K]  dtype: GDN_BF16, or GDN_F8E4M3 with
+ *   x_scale [M], w_scale [N] fp32 (both required in 8 bits, null in bf16), as
+ *            gdn_add_rmsnorm and gdn_quantize_rows write them
+ *   bias     [N] fp32, nullable
+ *   residual [M, N] out_dtype, nullable
+ *   y        [M, N] out_dtype: GDN_BF16 or GDN_F32; may be residual itself
+ *   z        [M, N] bf16, nullable: the activation's argument, for gdn_linear_bwd
+ * Products are exact and summed in fp32; each output is rounded once.  Large
+ * K with few tiles is summed in a fixed number of parts that depends on the
+ * sizes alone (fp32 partial sums in the workspace, added in order).
+ *   M, N >= 1, any value; K a multiple of 8 (bf16) or 16 (8 bits); N and K at
+ *   most 2^22 and ceil(M / 256) * ceil(N / 256) below 2^22
+ *   x, w and residual, y, z 16-byte aligned
+ *   ws  gdn_linear_workspace() bytes, 256-byte aligned (may be NULL if 0)
+ * Errors: GDN_ERR_INVALID_ARG (null required pointers, scales that do not
+ * belong, bad sizes, misalignment, an output overlapping an input, another
+ * output or the workspace), GDN_ERR_UNSUPPORTED (K not a multiple as above,
+ * sizes beyond the limits, types or activation not listed),
+ * GDN_ERR_WORKSPACE, GDN_ERR_HIP.  Asynchronous on `stream`.
+ */
+size_t gdn_linear_workspace(int M, int N, int K, gdn_dtype dtype);
+
+gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const float *w_scale, const float *bias,
+                      const void *residual, void *y, void *z, int M, int N, int K, gdn_dtype dtype,
+                      gdn_dtype out_dtype, gdn_act act, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * gdn_linear_bwd -- gradients of gdn_linear with bf16 x and w, for
+ * L = sum(dy . y) (the gradient of residual is dy itself):
+ *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum over rows of dz
+ *   dy [M, N] dy_dtype (GDN_BF16 or GDN_F32), 16-byte aligned
+ *   z  [M, N] bf16, 16-byte aligned: required with an activation, null without
+ *   dx [M, K], dw [N, K]  grad_dtype (GDN_BF16 or GDN_F32), 16-byte aligned, nullable
+ *   dbias [N] fp32, nullable
+ * dz takes part in the products as a bf16 operand.  With GDN_BF16 gradients
+ * it is rounded to bf16 (as its products' results are); with GDN_F32 it is
+ * kept exactly: dy itself where that is bf16 and there is no activation,
+ * otherwise as three bf16 parts that together carry its fp32 value (three
+ * times the products).  dbias sums the unrounded dz in a fixed order.
+ *   ws  gdn_linear_bwd_workspace() bytes (same sizes, types, activation and
+ *       set of outputs), 256-byte aligned (may be NULL if 0)
+ * Sizes as gdn_linear, with M * N limits for M * K and N * K too.  Errors as
+ * gdn_linear.
+ */
+size_t gdn_linear_bwd_workspace(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
+                                int need_dx, int need_dw, int need_dbias);
+
+gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,
+                          float *dbias, int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
+                          void *ws, size_t ws_bytes, void *stream);
+
 /*
  * gdn_clock_probe -- measurement aid, not part of the operation: enqueues
  * nblocks single-wave workgroups that each spin for spin_us microseconds of
