@@ -117,9 +117,15 @@ def _check(code: int, what: str):
         raise RuntimeError(f"{what} failed: {status_string(code)} (status {code})")
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t):
@@ -600,13 +606,14 @@ def gdn_gated_rmsnorm(o, z, weight, eps=1e-5, out=None):
     return y
 
 
-def _codes():
-    torch = _torch()
-    return {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_F8E4M3}
+_CODES = {}
 
 
 def _code(t, name):
-    code = _codes().get(t)
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_F8E4M3})
+    code = _CODES.get(t)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float8_e4m3fn, got {t}")
     return code
@@ -616,18 +623,31 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_device(fn, what, dev, args):
+def _scratch(nbytes, device):
+    """nbytes of 256-byte aligned workspace (torch's allocations are; a slice otherwise)."""
+    ws = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    return ws if ws.data_ptr() % 256 == 0 else _workspace(nbytes, device)[1]
+
+
+def _on_device(fn, what, dev, *args):
     """Calls fn(*args, stream) with dev as the current device, on its current stream."""
     torch = _torch()
     if dev.type != "cuda":
         raise ValueError(f"{what}: tensors must be on the GPU, got {dev}")
     if torch.cuda.current_device() == dev.index:
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            code = fn(*args, _raw_stream(dev))
     if code:
         _check(code, what)
+
+
+def _raw_stream(dev):
+    """Handle of torch's current stream on dev (the short way where this torch has it: 0.1 us against 1.9)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev.index) if get is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-5, out_dtype=None, return_rstd=False, out=None,
@@ -660,8 +680,8 @@ def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-5, out_dtype=None, return_r
     rstd = torch.empty(shape[:-1], dtype=f32, device=dev) if return_rstd else None
     y_scale = torch.empty(shape[:-1], dtype=f32, device=dev) if odt == torch.float8_e4m3fn else None
     _on_device(load().gdn_add_rmsnorm, "gdn_add_rmsnorm", dev,
-               (_addr(x), _addr(residual), _addr(weight), _addr(y), _addr(r), _addr(rstd), _addr(y_scale), rows, D,
-                _code(x.dtype, "x"), _code(rdt, "residual"), _code(odt, "out_dtype"), float(eps)))
+               _addr(x), _addr(residual), _addr(weight), _addr(y), _addr(r), _addr(rstd), _addr(y_scale), rows, D,
+                _code(x.dtype, "x"), _code(rdt, "residual"), _code(odt, "out_dtype"), float(eps))
     return y, r, rstd, y_scale
 
 
@@ -692,11 +712,11 @@ def gdn_add_rmsnorm_bwd(dy, r, weight, rstd, dr=None, need_dweight=True, workspa
     if need_dweight:
         dw = torch.empty((D,), dtype=f32, device=dev)
         need = lib.gdn_add_rmsnorm_bwd_workspace(rows, D)
-        ws = workspace if workspace is not None else _workspace(need, dev)[1]
+        ws = workspace if workspace is not None else _scratch(need, dev)
         nbytes = ws.numel() * ws.element_size()
     _on_device(lib.gdn_add_rmsnorm_bwd, "gdn_add_rmsnorm_bwd", dev,
-               (_addr(dy), _addr(r), _addr(weight), _addr(rstd), _addr(dr), _addr(dx), _addr(dw), rows, D,
-                _code(dy.dtype, "dy"), _code(r.dtype, "r"), _addr(ws), nbytes))
+               _addr(dy), _addr(r), _addr(weight), _addr(rstd), _addr(dr), _addr(dx), _addr(dw), rows, D,
+                _code(dy.dtype, "dy"), _code(r.dtype, "r"), _addr(ws), nbytes)
     return dx, dw
 
 
@@ -712,7 +732,7 @@ def gdn_quantize_rows(x):
     q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
     scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     _on_device(load().gdn_quantize_rows, "gdn_quantize_rows", dev,
-               (_addr(x), _addr(q), _addr(scale), x.numel() // D if D else 0, D, _code(x.dtype, "x")))
+               _addr(x), _addr(q), _addr(scale), x.numel() // D if D else 0, D, _code(x.dtype, "x"))
     return q, scale
 
 
@@ -767,12 +787,12 @@ def gdn_linear(x, weight, bias=None, residual=None, act="none", x_scale=None, w_
     if ws is None:
         need = lib.gdn_linear_workspace(M, N, K, code)
         if need:
-            ws = _workspace(need, dev)[1]
+            ws = _scratch(need, dev)
     if ws is not None:
         nbytes = ws.numel() * ws.element_size()
     _on_device(lib.gdn_linear, "gdn_linear", dev,
-               (_addr(x), _addr(weight), _addr(x_scale), _addr(w_scale), _addr(bias), _addr(residual), _addr(y),
-                _addr(z), M, N, K, code, ocode, _act_code(act), _addr(ws), nbytes))
+               _addr(x), _addr(weight), _addr(x_scale), _addr(w_scale), _addr(bias), _addr(residual), _addr(y),
+                _addr(z), M, N, K, code, ocode, _act_code(act), _addr(ws), nbytes)
     return y, z
 
 
@@ -812,12 +832,12 @@ def gdn_linear_bwd(dy, x, weight, z=None, act="none", bias=False, grad_dtype=Non
     if ws is None:
         need = lib.gdn_linear_bwd_workspace(M, N, K, dyc, gc, a, int(need_dx), int(need_dw), int(bool(bias)))
         if need:
-            ws = _workspace(need, dev)[1]
+            ws = _scratch(need, dev)
     if ws is not None:
         nbytes = ws.numel() * ws.element_size()
     _on_device(lib.gdn_linear_bwd, "gdn_linear_bwd", dev,
-               (_addr(dy), _addr(x), _addr(weight), _addr(z) if a else None, _addr(dx), _addr(dw), _addr(db), M, N, K,
-                dyc, gc, a, _addr(ws), nbytes))
+               _addr(dy), _addr(x), _addr(weight), _addr(z) if a else None, _addr(dx), _addr(dw), _addr(db), M, N, K,
+                dyc, gc, a, _addr(ws), nbytes)
     return dx, dw, db
 
 

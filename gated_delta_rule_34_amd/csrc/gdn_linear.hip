@@ -18,11 +18,30 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * LOG2E));
 }
 
+// Phi(z) of the normal distribution, and e = exp(-z^2 / 2): the upper tail
+// Q(|z|) = e t (b1 + b2 t + .. + b5 t^4) with t = 1 / (1 + p |z|), the rational
+// form 26.2.17 of Abramowitz and Stegun's handbook (absolute error 7.5e-8, about
+// the fp32 spacing of values from 1/2 on; no cancellation for z < 0).
+// About 15 instructions, against 40 of the library's erf.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.2316419f, fabsf(z), 1.f));
+    e = __builtin_amdgcn_exp2f(z * z * (-0.5f * LOG2E));
+    float p = fmaf(t, 1.330274429f, -1.821255978f);
+    p = fmaf(t, p, 1.781477937f);
+    p = fmaf(t, p, -0.356563782f);
+    p = fmaf(t, p, 0.319381530f);
+    const float q = 0.3989422804014327f * e * (t * p);
+    return z < 0.f ? q : 1.f - q;
+}
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
     switch (act) {
         case ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
         case ACT_SILU: return z * sigmoid_fast(z);
-        case ACT_GELU: return z * (0.5f * (1.f + erff(z * 0.70710678118654752f)));
+        case ACT_GELU: {
+            float e;
+            return z * normal_cdf(z, e);
+        }
     }
     return z;
 }
@@ -34,9 +53,11 @@ __device__ __forceinline__ float act_bwd(int act, float z) {
             const float p = sigmoid_fast(z);
             return p * (1.f + z * (1.f - p));
         }
-        case ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
-                   z * __builtin_amdgcn_exp2f(-0.5f * LOG2E * z * z) * 0.3989422804014327f;
+        case ACT_GELU: {
+            float e;
+            const float c = normal_cdf(z, e);
+            return c + z * e * 0.3989422804014327f;
+        }
     }
     return 1.f;
 }
@@ -50,34 +71,93 @@ struct Epilogue {
     long ld;        // columns of y, residual and z
     int act;
     bool y32;
-    __device__ __forceinline__ void operator()(float (&v)[8], long i, int j, int J) const {
+    // What columns j .. j + 7 share over all rows, and what a row adds.
+    struct Cols {
+        f32x8 s, b;
+    };
+    struct Row {
+        float a;
+        u32x4 r0, r1;  // residual: eight bf16, or eight fp32
+    };
+    __device__ __forceinline__ Cols cols(int j, int J) const {
+        Cols c;
+        if (xs) c.s = load8v(ws, j, J);
+        if (bias) c.b = load8v(bias, j, J);
+        return c;
+    }
+    // only for j + 8 <= J
+    __device__ __forceinline__ Row row(long i, int j) const {
+        Row o;
+        if (xs) o.a = xs[i];
+        if (residual) {
+            if (y32) {
+                const u32x4_a2 *p = (const u32x4_a2 *)((const float *)residual + i * ld + j);
+                o.r0 = p[0];
+                o.r1 = p[1];
+            } else {
+                o.r0 = *(const u32x4_a2 *)((const uint16_t *)residual + i * ld + j);
+            }
+        }
+        return o;
+    }
+    __device__ __forceinline__ f32x8 before(f32x8 v, const Cols &c, float a) const {
         if (xs) {
-            float s[8];
-            load_piece(s, ws, j, J);
-            const float a = xs[i];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= a * s[e];
+            for (int e = 0; e < 8; ++e) v[e] *= a * c.s[e];
         }
         if (bias) {
-            float b[8];
-            load_piece(b, bias, j, J);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += b[e];
+            for (int e = 0; e < 8; ++e) v[e] += c.b[e];
         }
-        if (z) store_piece(z + i * ld, v, j, J);
-        if (act != ACT_NONE) {
+        return v;
+    }
+    __device__ __forceinline__ f32x8 activate(f32x8 v) const {
+        if (act == ACT_RELU) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = act_fwd(act, v[e]);
+            for (int e = 0; e < 8; ++e) v[e] = act_fwd(ACT_RELU, v[e]);
+        } else if (act == ACT_SILU) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = act_fwd(ACT_SILU, v[e]);
+        } else if (act == ACT_GELU) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = act_fwd(ACT_GELU, v[e]);
         }
+        return v;
+    }
+    // whole pieces (j + 8 <= J), with what cols() and row() fetched
+    __device__ __forceinline__ void whole(f32x8 v, const Cols &c, const Row &o, long i, int j) const {
+        v = before(v, c, o.a);
+        if (z) store8v(z + i * ld + j, v);
+        v = activate(v);
         if (residual) {
-            float t[8];
-            if (y32) load_piece(t, (const float *)residual + i * ld, j, J);
-            else load_piece(t, (const uint16_t *)residual + i * ld, j, J);
+            if (y32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] += __uint_as_float(o.r0[e]);
+                    v[4 + e] += __uint_as_float(o.r1[e]);
+                }
+            } else {
+                const f32x8 t = bf16x8_to_f32(o.r0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += t[e];
+            }
+        }
+        if (y32) store8v((float *)y + i * ld + j, v);
+        else store8v((uint16_t *)y + i * ld + j, v);
+    }
+    // any piece that begins in the row
+    __device__ __forceinline__ void any(f32x8 v, long i, int j, int J) const {
+        v = before(v, cols(j, J), xs ? xs[i] : 0.f);
+        if (z) store8v(z + i * ld, v, j, J);
+        v = activate(v);
+        if (residual) {
+            const f32x8 t = y32 ? load8v((const float *)residual + i * ld, j, J)
+                                : load8v((const uint16_t *)residual + i * ld, j, J);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += t[e];
         }
-        if (y32) store_piece((float *)y + i * ld, v, j, J);
-        else store_piece((uint16_t *)y + i * ld, v, j, J);
+        if (y32) store8v((float *)y + i * ld, v, j, J);
+        else store8v((uint16_t *)y + i * ld, v, j, J);
     }
 };
 
@@ -163,8 +243,10 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
         };
         auto mul = [&](auto set, int x) {
             constexpr int h = decltype(set)::value;
+            __builtin_amdgcn_s_setprio(1);  // before the other wave's reads and loads: 2 %
 #pragma unroll
             for (int y = 0; y < NI; ++y) acc[x][y] = mma_bf16_raw(acc[x][y], fu[h][x], fv[h][y]);
+            __builtin_amdgcn_s_setprio(0);
         };
         static_assert(NI <= NJ && (LV + LU) % NJ == 0, "shares");
         constexpr int PER = (LV + LU) / NJ;
@@ -256,29 +338,71 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
 
     // Epilogue: 16 rows of the wave's part of the tile at a time through LDS
     // (its own region), so that a lane holds eight consecutive columns and a
-    // row's stores are contiguous.
+    // row's stores are contiguous.  Where the tile's columns are whole, what
+    // the rows add is fetched ahead of the products' way through LDS.
     __syncthreads();
     float *img = (float *)smem + wave * 16 * LDJ;
-    constexpr int LPR = NJ * 2, RPP = 64 / LPR;    // lanes per row, rows per pass
+    constexpr int LPR = NJ * 2, RPP = 64 / LPR, Q = 16 / RPP;  // lanes per row, rows per pass, passes
     const int r = lane & 15, g = lane >> 4, c8 = (lane % LPR) * 8, rr = lane / LPR;
-    const int j = j0 + wj + c8;
+    const int j = j0 + wj + c8, ib = i0 + wi + rr;
+    // (the loops below stay loops: unrolled, the code no longer fits the
+    // instruction cache and a pass costs a fetch from L2 per line, measured
+    // 514 against 371 us at 32768 x 4096 x 1024)
+    auto put = [&](int y) {
 #pragma unroll
-    for (int y = 0; y < NI; ++y) {
+        for (int k = 0; k < NI; ++k) {
+            if (k == y) {
 #pragma unroll
-        for (int x = 0; x < NJ; ++x) *(f32x4 *)(img + r * LDJ + 16 * x + 4 * g) = acc[x][y];
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int q = 0; q < 16 / RPP; ++q) {
-            const int i = i0 + wi + 16 * y + q * RPP + rr;
-            const float *src = img + (q * RPP + rr) * LDJ + c8;
-            const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 4);
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            if (i < a.I && j < a.J) {
-                if (part) store_piece(part + ((long)blockIdx.y * a.I + i) * a.J, v, j, a.J);
-                else ep(v, i, j, a.J);
+                for (int x = 0; x < NJ; ++x) *(f32x4 *)(img + r * LDJ + 16 * x + 4 * g) = acc[x][k];
+                // distinct per case: merged, the accumulators would be
+                // indexed at run time, that is, moved to scratch memory
+                asm volatile("; rows %0" ::"n"(k));
             }
         }
-        __builtin_amdgcn_wave_barrier();
+    };
+    auto get = [&](int q) {
+        const float *src = img + (q * RPP + rr) * LDJ + c8;
+        const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 4);
+        return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    if (part) {
+        part += (long)blockIdx.y * a.I * a.J;
+#pragma unroll 1
+        for (int y = 0; y < NI; ++y) {
+            put(y);
+#pragma unroll 1
+            for (int q = 0; q < Q; ++q) {
+                const int i = ib + 16 * y + q * RPP;
+                const f32x8 v = get(q);
+                if (i < a.I && j < a.J) store8v(part + (long)i * a.J, v, j, a.J);
+            }
+        }
+    } else if (j0 + BJ <= a.J) {
+        const Epilogue::Cols c = ep.cols(j, a.J);
+#pragma unroll 1
+        for (int y = 0; y < NI; ++y) {
+            Epilogue::Row o[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) o[q] = ep.row(min(ib + 16 * y + q * RPP, a.I - 1), j);
+            put(y);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = ib + 16 * y + q * RPP;
+                const f32x8 v = get(q);
+                if (i < a.I) ep.whole(v, c, o[q], i, j);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int y = 0; y < NI; ++y) {
+            put(y);
+#pragma unroll 1
+            for (int q = 0; q < Q; ++q) {
+                const int i = ib + 16 * y + q * RPP;
+                const f32x8 v = get(q);
+                if (i < a.I && j < a.J) ep.any(v, i, j, a.J);
+            }
+        }
     }
 }
 
@@ -289,19 +413,242 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, Epilogu
     for (long u = (long)blockIdx.x * 256 + threadIdx.x; u < n; u += (long)gridDim.x * 256) {
         const long i = u / pieces;
         const int j = (int)(u - i * pieces) * 8;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int s = 0; s < splits; ++s) {
-            float t[8];
-            load_piece(t, part + ((long)s * I + i) * J, j, J);
+            const f32x8 t = load8v(part + ((long)s * I + i) * J, j, J);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += t[e];
         }
-        ep(v, i, j, J);
+        ep.any(v, i, j, J);
+    }
+}
+
+// Few rows (decode): every weight is read once and used for at most 16 MT
+// rows, so the product is bound by that read.  A workgroup owns 16 NB columns;
+// its W waves take turns along k in pieces of RB bytes per row.  A wave brings
+// its piece of the weight rows and of the rows of x into its own part of LDS,
+// whole rows' pieces per instruction: fragments loaded directly would touch 16
+// rows at once, which a power-of-two row length puts on one memory channel
+// (64 x 64 x 4096 in bf16: 19.8 us so, 8.1 us this way).  Waves do
+// not wait for each other until their sums meet in LDS, where they are added
+// in order.  One launch, no workspace.  1 x 4096 x 4096 in bf16: 8.7 us in a
+// graph, 3.9 TB/s of weights; 1 x 4096 x 16384: 30.9 us, 4.3 TB/s.  e4m3 is converted to bf16 fragments
+// for every output type (the conversion hides behind the loads).
+template <int NB, int MT, int W, int RB, bool F8>
+__global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w, int I, int J, int K, Epilogue ep) {
+    constexpr int ES = F8 ? 1 : 2;
+    constexpr int RPL = 1024 / RB;              // rows per load instruction
+    constexpr int UNITS = RB / 16;              // 16-byte units per row piece
+    constexpr int WB = 16 * NB * RB, XB = 16 * MT * RB;
+    constexpr int LDR = 16 * NB + 4;            // floats per row of a wave's sums
+    constexpr int SB = W * 16 * MT * LDR * 4;
+    constexpr int PIECES = 2 * NB * 16 * MT;
+    __shared__ __attribute__((aligned(1024))) char smem[W * (WB + XB) > SB ? W * (WB + XB) : SB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int j0 = blockIdx.x * 16 * NB;
+    const uint32_t row = (uint32_t)K * ES;
+    // what the epilogue's threads will need
+    const int pi = threadIdx.x / (2 * NB), pj = j0 + 8 * (threadIdx.x % (2 * NB));
+    const bool mine = threadIdx.x < PIECES && pi < I && pj < J, full = pj + 8 <= J;
+    Epilogue::Cols ec;
+    Epilogue::Row er;
+    if (PIECES <= W * 64 && mine && full) {
+        ec = ep.cols(pj, J);
+        er = ep.row(pi, pj);
+    }
+    f32x4 acc[NB][MT];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = zero4();
+
+    lds_cchar *wl = (lds_cchar *)smem + wave * (WB + XB), *xl = wl + WB;
+    const uint32_t lw = (uint32_t)(uintptr_t)wl, lx = lw + WB;
+    const char *wb = w + (long)j0 * row;
+    const uint32_t wr = (uint32_t)min(16 * NB, J - j0) * row, xr = (uint32_t)I * row;
+    // unit c of row k of a piece lies at c ^ (2 swz_col(k)): the rows of a
+    // fragment read fall on different banks
+    const int lr = lane / UNITS;
+    for (int p = wave; p * RB < (int)row; p += W) {
+        const int left = (int)row - p * RB;
+        const i32x4 rw = make_rsrc(wb + (long)p * RB, wr), rx = make_rsrc(x + (long)p * RB, xr);
+#pragma unroll
+        for (int n = 0; n < 16 * NB / RPL; ++n) {
+            const int k = n * RPL + lr, c = ((lane % UNITS) ^ (swz_col(k & 15) << 1)) * 16;
+            lds_load(lw + n * 1024, c < left ? (uint32_t)k * row + c : kOutOfRange, rw);
+        }
+#pragma unroll
+        for (int n = 0; n < 16 * MT / RPL; ++n) {
+            const int k = n * RPL + lr, c = ((lane % UNITS) ^ (swz_col(k & 15) << 1)) * 16;
+            if (n * RPL < I)  // rows past I: left as they are, their sums are not used
+                lds_load(lx + n * 1024, c < left ? (uint32_t)k * row + c : kOutOfRange, rx);
+        }
+        mm_wait<0>();
+        typedef __attribute__((address_space(3))) const u32x4 lds_v;
+#pragma unroll
+        for (int u = 0; u < RB / 64; ++u) {
+            const int at = r * RB + ((4 * u + g) ^ (swz_col(r) << 1)) * 16;
+            u32x4 fw[NB], fx[MT];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) fw[n] = *(lds_v *)(wl + at + n * 16 * RB);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fx[m] = *(lds_v *)(xl + at + m * 16 * RB);
+            if constexpr (F8) {
+                u32x4 bx[MT][2];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) f8_to_bf16(bx[m], fx[m]);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    u32x4 bw[2];
+                    f8_to_bf16(bw, fw[n]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        acc[n][m] = mma_bf16_raw(acc[n][m], bw[0], bx[m][0]);
+                        acc[n][m] = mma_bf16_raw(acc[n][m], bw[1], bx[m][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[n][m] = mma_bf16_raw(acc[n][m], fw[n], fx[m]);
+            }
+        }
+        mm_wait<0>();  // this piece's reads are done before the next one's loads
+    }
+    __syncthreads();
+    typedef float Sums[16 * MT][LDR];
+    Sums *sums = (Sums *)smem;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) *(f32x4 *)&sums[wave][16 * m + r][16 * n + 4 * g] = acc[n][m];
+    __syncthreads();
+    for (int q = threadIdx.x; q < PIECES; q += W * 64) {
+        const int i = q / (2 * NB), c = 8 * (q % (2 * NB)), j = j0 + c;
+        if (i >= I || j >= J) continue;
+        f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < W; ++p) {
+            const f32x4 lo = *(const f32x4 *)&sums[p][i][c], hi = *(const f32x4 *)&sums[p][i][c + 4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += lo[e];
+                v[4 + e] += hi[e];
+            }
+        }
+        if (PIECES <= W * 64 && full) ep.whole(v, ec, er, i, j);
+        else ep.any(v, i, j, J);
     }
 }
 
 // What rounding left of d (nothing of an infinity or NaN: the first plane holds it).
 __device__ __forceinline__ float rest(float d, float hi) { return fabsf(hi) < __builtin_inff() ? d - hi : 0.f; }
+
+// Few rows (decode): every weight is read once and used for at most 16 MT
+// rows, so the product is bound by that read.  A workgroup owns 16 NB columns;
+// its W waves split k and read their part of the weight rows straight into
+// MFMA fragments, U loads in flight each, with the rows of x beside them from
+// L2; the waves' sums meet in LDS and are added in order.  One launch, no
+// workspace.  e4m3 is converted to bf16 fragments for every output type (the
+// conversion hides behind the loads).
+template <int NB, int MT, int W, bool F8>
+__global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w, int I, int J, int K, Epilogue ep) {
+    constexpr int U = MT == 1 ? 8 : 4;          // slabs in flight
+    constexpr int CH = F8 ? 16 : 8, SLAB = 4 * CH;  // values of k per lane and per slab
+    constexpr int ES = F8 ? 1 : 2;
+    constexpr int LDR = 16 * NB + 4;            // floats per row of a wave's sums
+    __shared__ __attribute__((aligned(16))) float sums[W][16 * MT][LDR];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int j0 = blockIdx.x * 16 * NB;
+    const long row = (long)K * ES;
+    const char *wp[NB], *xp[MT];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) wp[n] = w + (long)min(j0 + 16 * n + r, J - 1) * row;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xp[m] = x + (long)min(16 * m + r, I - 1) * row;
+    // what the epilogue's threads will need
+    constexpr int PIECES = 2 * NB * 16 * MT;
+    const int pi = threadIdx.x / (2 * NB), pj = j0 + 8 * (threadIdx.x % (2 * NB));
+    const bool mine = threadIdx.x < PIECES && pi < I && pj < J, full = pj + 8 <= J;
+    Epilogue::Cols ec;
+    Epilogue::Row er;
+    if (PIECES <= W * 64 && mine && full) {
+        ec = ep.cols(pj, J);
+        er = ep.row(pi, pj);
+    }
+    f32x4 acc[NB][MT];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = zero4();
+    const int slabs = (K + SLAB - 1) / SLAB, per = (slabs + W - 1) / W;
+    const int s0 = wave * per, s1 = min(s0 + per, slabs);
+    for (int s = s0; s < s1; s += U) {
+        u32x4 fw[U][NB], fx[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (s + u) * SLAB + CH * g;
+            const bool in = s + u < s1 && k < K;
+            const long o = in ? (long)k * ES : 0;  // out of range: the row's start, not used
+#pragma unroll
+            for (int n = 0; n < NB; ++n) fw[u][n] = *(const u32x4 *)(wp[n] + o);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fx[u][m] = *(const u32x4 *)(xp[m] + o);
+            if (!in) {  // both zero: an infinity times zero would not be
+#pragma unroll
+                for (int n = 0; n < NB; ++n) fw[u][n] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int m = 0; m < MT; ++m) fx[u][m] = u32x4{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (F8) {
+                u32x4 bx[MT][2];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) f8_to_bf16(bx[m], fx[u][m]);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    u32x4 bw[2];
+                    f8_to_bf16(bw, fw[u][n]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        acc[n][m] = mma_bf16_raw(acc[n][m], bw[0], bx[m][0]);
+                        acc[n][m] = mma_bf16_raw(acc[n][m], bw[1], bx[m][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[n][m] = mma_bf16_raw(acc[n][m], fw[u][n], fx[u][m]);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) *(f32x4 *)&sums[wave][16 * m + r][16 * n + 4 * g] = acc[n][m];
+    __syncthreads();
+    for (int q = threadIdx.x; q < PIECES; q += W * 64) {
+        const int i = q / (2 * NB), c = 8 * (q % (2 * NB)), j = j0 + c;
+        if (i >= I || j >= J) continue;
+        f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < W; ++p) {
+            const f32x4 lo = *(const f32x4 *)&sums[p][i][c], hi = *(const f32x4 *)&sums[p][i][c + 4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += lo[e];
+                v[4 + e] += hi[e];
+            }
+        }
+        if (PIECES <= W * 64 && full) ep.whole(v, ec, er, i, j);
+        else ep.any(v, i, j, J);
+    }
+}
 
 // dz = dy act'(z) in `planes` bf16 planes (rounded; what is left of it; what
 // is left of that) of Jp columns, Jp a multiple of 8, zero past J; and the
@@ -383,6 +730,36 @@ static size_t mm_part_bytes(const MmPlan &p, int I, int J) {
     return p.splits > 1 ? (size_t)p.splits * I * J * sizeof(float) : 0;
 }
 
+// The few-rows kernel takes up to kMvRows rows.
+constexpr int kMvRows = 64;
+
+template <bool F8>
+static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, const Epilogue &ep, hipStream_t st) {
+#define GDN_MV(NBv, MTv, Wv, RBv)                                                                                  \
+    hipLaunchKernelGGL((mv_kernel<NBv, MTv, Wv, RBv, F8>), dim3((unsigned)((N + 16 * NBv - 1) / (16 * NBv))),      \
+                       dim3(Wv * 64), 0, st, (const char *)x, (const char *)w, M, N, K, ep)
+    // Up to 512 workgroups of 16 columns run in one or two rounds; more columns
+    // go 32 to a workgroup, which reads x half as often (17 x 16384 x 1024 in
+    // bf16: 8.8 against 13.5 us; 17 x 4096 x 4096: 10.2 against 15.9 the other
+    // way round).  One row tile's pieces are 256 bytes, which leaves room for
+    // two workgroups in a compute unit; rows of 16 KB and more bring 512 at a
+    // time (1 x 4096 x 16384: 30.9 against 34.2 us; 1 x 16384 x 1024: 9.1
+    // against 12.6 the other way round).
+    const bool wide = N > 512 * 16;
+    if (M <= 16) {
+        if ((long)K * (F8 ? 1 : 2) >= 16384 && !wide) GDN_MV(1, 1, 8, 512);
+        else GDN_MV(1, 1, 8, 256);
+    } else if (M <= 32) {
+        if (wide) GDN_MV(2, 2, 4, 256);
+        else GDN_MV(1, 2, 8, 256);
+    } else {
+        if (wide) GDN_MV(2, 4, 4, 256);
+        else GDN_MV(1, 4, 7, 256);
+    }
+#undef GDN_MV
+    return hipGetLastError();
+}
+
 template <bool TV, bool TU, int MODE>
 static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t st) {
     const int slab = MODE == MM_BF16 ? 64 : 128;
@@ -408,7 +785,10 @@ static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t 
 
 static int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
 
-size_t linear_ws_bytes(int M, int N, int K, bool f8) { return mm_part_bytes(mm_plan(M, N, slabs_of(K, f8)), M, N); }
+size_t linear_ws_bytes(int M, int N, int K, bool f8) {
+    if (M <= kMvRows) return 0;
+    return mm_part_bytes(mm_plan(M, N, slabs_of(K, f8)), M, N);
+}
 
 hipError_t launch_linear(const void *x, const void *w, const float *xs, const float *ws, const float *bias,
                          const void *residual, void *y, void *z, int M, int N, int K, bool f8, bool y_f32, int act,
@@ -419,6 +799,8 @@ hipError_t launch_linear(const void *x, const void *w, const float *xs, const fl
     a.ldv = a.ldu = K * es;
     a.I = M; a.J = N; a.K = K; a.parts = 1;
     const Epilogue ep{xs, ws, bias, residual, y, (uint16_t *)z, N, act, y_f32};
+    if (M <= kMvRows)
+        return f8 ? mv_run<true>(x, w, M, N, K, ep, st) : mv_run<false>(x, w, M, N, K, ep, st);
     if (!f8) return mm_run<false, false, MM_BF16>(a, ep, part, st);
     return y_f32 ? mm_run<false, false, MM_F8_F32>(a, ep, part, st) : mm_run<false, false, MM_F8>(a, ep, part, st);
 }

@@ -68,6 +68,56 @@ __device__ __forceinline__ void store_piece(float *p, const float (&v)[8], int c
     }
 }
 
+// The same on a native vector (kept in registers where an array that is passed
+// around can end up in scratch memory), whole pieces and any piece.
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x8 bf16x8_to_f32(const u32x4 &u) {
+    f32x8 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(u[e] << 16);
+        v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+    return v;
+}
+__device__ __forceinline__ f32x8 load8v(const float *p) {
+    const f32x4_a4 a = *(const f32x4_a4 *)p, b = *(const f32x4_a4 *)(p + 4);
+    return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+__device__ __forceinline__ f32x8 load8v(const uint16_t *p) { return bf16x8_to_f32(*(const u32x4_a2 *)p); }
+__device__ __forceinline__ void store8v(uint16_t *p, const f32x8 &v) {
+    u32x4_a2 u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = pack2_bf16(v[2 * e], v[2 * e + 1]);
+    *(u32x4_a2 *)p = u;
+}
+__device__ __forceinline__ void store8v(float *p, const f32x8 &v) {
+    *(f32x4_a4 *)p = f32x4_a4{v[0], v[1], v[2], v[3]};
+    *(f32x4_a4 *)(p + 4) = f32x4_a4{v[4], v[5], v[6], v[7]};
+}
+template <class T>
+__device__ __forceinline__ f32x8 load8v(const T *p, int c, int D) {
+    if (c + 8 <= D) return load8v(p + c);
+    f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e < D) v[e] = load_elem(p + c + e);
+    return v;
+}
+__device__ __forceinline__ void store_elem(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_elem(uint16_t *p, float v) { *p = to_bf16(v); }
+template <class T>
+__device__ __forceinline__ void store8v(T *p, const f32x8 &v, int c, int D) {
+    if (c + 8 <= D) {
+        store8v(p + c, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c + e < D) store_elem(p + c + e, v[e]);
+}
+
 // v / scale for one row: a reciprocal and one correction step, which gives the
 // correctly rounded quotient that a division would (codes are compared with
 // it, and quotients of bf16 values fall on e4m3's midpoints often); scales
