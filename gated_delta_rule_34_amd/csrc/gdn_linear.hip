@@ -127,7 +127,7 @@ struct Epilogue {
     // whole pieces (j + 8 <= J), with what cols() and row() fetched
     __device__ __forceinline__ void whole(f32x8 v, const Cols &c, const Row &o, long i, int j) const {
         v = before(v, c, o.a);
-        if (z) store8v(z + i * ld + j, v);
+        if (z) store8nt(z + i * ld + j, v);  // read again in the backward only
         v = activate(v);
         if (residual) {
             if (y32) {
@@ -168,9 +168,9 @@ struct Epilogue {
 // to bf16, which holds them exactly, as they leave LDS.
 enum { MM_BF16 = 0, MM_F8 = 1, MM_F8_F32 = 2 };
 
-// Grid: x = tiles, y = splits of k.  part (nullable): fp32 partial sums
+// Grid: x = tiles, y = splits of k.  NBUF slabs in LDS.  part (nullable): fp32 partial sums
 // [split, I, J] instead of the epilogue.
-template <int BI, int BJ, int WI, int WJ, bool TV, bool TU, int MODE>
+template <int BI, int BJ, int WI, int WJ, int NBUF, bool TV, bool TU, int MODE>
 __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, float *part) {
     constexpr bool F8 = MODE != MM_BF16;
     constexpr int W = WI * WJ, NI = BI / WI / 16, NJ = BJ / WJ / 16;  // 16-wide tiles per wave
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
     constexpr int BUF = SV::kBytes + SU::kBytes;
     constexpr int LDJ = BJ / WJ + 4;               // floats per row of the epilogue's image
     constexpr int EPI = W * 16 * LDJ * 4;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * BUF > EPI ? 2 * BUF : EPI];
+    __shared__ __attribute__((aligned(1024))) char smem[NBUF * BUF > EPI ? NBUF * BUF : EPI];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int bi, bj;
     mm_tile(blockIdx.x, a.ti, a.tj, bi, bj);
@@ -231,9 +231,9 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
         // Fragments are read half a slab ahead of their products, in two
         // register sets, so the MFMAs only wait where waves meet: in the
         // middle of slab t every wave holds the last of t in registers, slab
-        // t + 1 has landed, and the loads of t + 2 go into t's buffer.  Past
-        // the end the loads write zeros and the reads are not used, which
-        // keeps the loop free of branches.
+        // t + 1 has landed, and the loads of t + NBUF go into t's buffer.
+        // Past the end the loads write zeros and the reads are not used,
+        // which keeps the loop free of branches.
         u32x4 fv[2][NI], fu[2][NJ];
         auto read = [&](auto set, int buf, int x) {  // x-th share of a set's reads
             constexpr int h = decltype(set)::value;
@@ -243,26 +243,25 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
         };
         auto mul = [&](auto set, int x) {
             constexpr int h = decltype(set)::value;
-            __builtin_amdgcn_s_setprio(1);  // before the other wave's reads and loads: 2 %
+            if (W == 8) __builtin_amdgcn_s_setprio(1);  // before the other wave's reads and loads: 2 %
 #pragma unroll
             for (int y = 0; y < NI; ++y) acc[x][y] = mma_bf16_raw(acc[x][y], fu[h][x], fv[h][y]);
-            __builtin_amdgcn_s_setprio(0);
+            if (W == 8) __builtin_amdgcn_s_setprio(0);
         };
-        static_assert(NI <= NJ && (LV + LU) % NJ == 0, "shares");
-        constexpr int PER = (LV + LU) / NJ;
+        static_assert(NI <= NJ, "shares");
         constexpr std::integral_constant<int, 0> h0;
         constexpr std::integral_constant<int, 1> h1;
         if (s0 < s1) {
-            load(0);
-            load(1);
-            mm_wait<LV + LU>();
+#pragma unroll
+            for (int n = 0; n < NBUF; ++n) load(n);
+            mm_wait<(NBUF - 1) * (LV + LU)>();
             __builtin_amdgcn_s_barrier();
             mm_fence();
 #pragma unroll
             for (int x = 0; x < NJ; ++x) read(h0, 0, x);
         }
+        int buf = 0;
         for (int t = s0; t < s1; ++t) {
-            const int buf = (t - s0) & 1;
 #pragma unroll
             for (int x = 0; x < NJ; ++x) {
                 // (the first products go first: the wait for their operands,
@@ -276,30 +275,35 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
             }
             __builtin_amdgcn_sched_barrier(0);
             begin();
-            mm_wait<0>();
+            mm_wait<(NBUF - 2) * (LV + LU)>();
             __builtin_amdgcn_s_barrier();
             mm_fence();
+            const int after = buf + 1 < NBUF ? buf + 1 : 0;
 #pragma unroll
             for (int x = 0; x < NJ; ++x) {
                 __builtin_amdgcn_sched_barrier(0);
-                read(h0, buf ^ 1, x);
+                read(h0, after, x);
 #pragma unroll
-                for (int n = 0; n < PER; ++n) piece(buf, x * PER + n);
+                for (int n = x * (LV + LU) / NJ; n < (x + 1) * (LV + LU) / NJ; ++n) piece(buf, n);
                 __builtin_amdgcn_sched_barrier(0);
                 mul(h1, x);
             }
+            buf = after;
         }
         mm_wait<0>();  // the loads past the end have written before LDS is used again
     } else {
-        if (s0 < s1) load(0);
+        if (s0 < s1) {
+#pragma unroll
+            for (int n = 0; n < NBUF - 1; ++n) load(n);
+        }
+        int buf = 0;
         for (int t = s0; t < s1; ++t) {
             // this slab's loads have landed (each wave its own), and every
-            // wave is done with the other buffer
-            mm_wait<0>();
+            // wave is done with the buffer that the next ones go to
+            mm_wait<(NBUF - 2) * (LV + LU)>();
             __builtin_amdgcn_s_barrier();
             mm_fence();
-            const int buf = (t - s0) & 1;
-            load(buf ^ 1);
+            load(buf > 0 ? buf - 1 : NBUF - 1);
             lds_cchar *iv = lds + buf * BUF, *iu = iv + SV::kBytes;
             if constexpr (MODE == MM_F8) {
                 i32x8 fv[NI];
@@ -332,6 +336,7 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
                     }
                 }
             }
+            buf = buf + 1 < NBUF ? buf + 1 : 0;
         }
         mm_wait<0>();
     }
@@ -423,9 +428,9 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, Epilogu
     }
 }
 
-// Few rows (decode): every weight is read once and used for at most 16 MT
-// rows, so the product is bound by that read.  A workgroup owns 16 NB columns;
-// its W waves take turns along k in pieces of RB bytes per row.  A wave brings
+// Few rows (decode) or few columns (gate projections): every weight, or every
+// row of x, is read once and used for at most 64 products, so the product is
+// bound by that read.  A workgroup owns 16 MT rows and 16 NB columns; its W waves take turns along k in pieces of RB bytes per row.  A wave brings
 // its piece of the weight rows and of the rows of x into its own part of LDS,
 // whole rows' pieces per instruction: fragments loaded directly would touch 16
 // rows at once, which a power-of-two row length puts on one memory channel
@@ -446,16 +451,17 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
     __shared__ __attribute__((aligned(1024))) char smem[W * (WB + XB) > SB ? W * (WB + XB) : SB];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int j0 = blockIdx.x * 16 * NB;
+    const int j0 = blockIdx.x * 16 * NB, i0 = blockIdx.y * 16 * MT;
+    const int rows = min(16 * MT, I - i0);
     const uint32_t row = (uint32_t)K * ES;
     // what the epilogue's threads will need
     const int pi = threadIdx.x / (2 * NB), pj = j0 + 8 * (threadIdx.x % (2 * NB));
-    const bool mine = threadIdx.x < PIECES && pi < I && pj < J, full = pj + 8 <= J;
+    const bool mine = threadIdx.x < PIECES && pi < rows && pj < J, full = pj + 8 <= J;
     Epilogue::Cols ec;
     Epilogue::Row er;
     if (PIECES <= W * 64 && mine && full) {
         ec = ep.cols(pj, J);
-        er = ep.row(pi, pj);
+        er = ep.row(i0 + pi, pj);
     }
     f32x4 acc[NB][MT];
 #pragma unroll
@@ -465,14 +471,14 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
 
     lds_cchar *wl = (lds_cchar *)smem + wave * (WB + XB), *xl = wl + WB;
     const uint32_t lw = (uint32_t)(uintptr_t)wl, lx = lw + WB;
-    const char *wb = w + (long)j0 * row;
-    const uint32_t wr = (uint32_t)min(16 * NB, J - j0) * row, xr = (uint32_t)I * row;
+    const char *wb = w + (long)j0 * row, *xb = x + (long)i0 * row;
+    const uint32_t wr = (uint32_t)min(16 * NB, J - j0) * row, xr = (uint32_t)rows * row;
     // unit c of row k of a piece lies at c ^ (2 swz_col(k)): the rows of a
     // fragment read fall on different banks
     const int lr = lane / UNITS;
     for (int p = wave; p * RB < (int)row; p += W) {
         const int left = (int)row - p * RB;
-        const i32x4 rw = make_rsrc(wb + (long)p * RB, wr), rx = make_rsrc(x + (long)p * RB, xr);
+        const i32x4 rw = make_rsrc(wb + (long)p * RB, wr), rx = make_rsrc(xb + (long)p * RB, xr);
 #pragma unroll
         for (int n = 0; n < 16 * NB / RPL; ++n) {
             const int k = n * RPL + lr, c = ((lane % UNITS) ^ (swz_col(k & 15) << 1)) * 16;
@@ -481,7 +487,7 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
 #pragma unroll
         for (int n = 0; n < 16 * MT / RPL; ++n) {
             const int k = n * RPL + lr, c = ((lane % UNITS) ^ (swz_col(k & 15) << 1)) * 16;
-            if (n * RPL < I)  // rows past I: left as they are, their sums are not used
+            if (n * RPL < rows)  // rows past I: left as they are, their sums are not used
                 lds_load(lx + n * 1024, c < left ? (uint32_t)k * row + c : kOutOfRange, rx);
         }
         mm_wait<0>();
@@ -527,7 +533,7 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
     __syncthreads();
     for (int q = threadIdx.x; q < PIECES; q += W * 64) {
         const int i = q / (2 * NB), c = 8 * (q % (2 * NB)), j = j0 + c;
-        if (i >= I || j >= J) continue;
+        if (i >= rows || j >= J) continue;
         f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < W; ++p) {
@@ -538,117 +544,13 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
                 v[4 + e] += hi[e];
             }
         }
-        if (PIECES <= W * 64 && full) ep.whole(v, ec, er, i, j);
-        else ep.any(v, i, j, J);
+        if (PIECES <= W * 64 && full) ep.whole(v, ec, er, i0 + i, j);
+        else ep.any(v, i0 + i, j, J);
     }
 }
 
 // What rounding left of d (nothing of an infinity or NaN: the first plane holds it).
 __device__ __forceinline__ float rest(float d, float hi) { return fabsf(hi) < __builtin_inff() ? d - hi : 0.f; }
-
-// Few rows (decode): every weight is read once and used for at most 16 MT
-// rows, so the product is bound by that read.  A workgroup owns 16 NB columns;
-// its W waves split k and read their part of the weight rows straight into
-// MFMA fragments, U loads in flight each, with the rows of x beside them from
-// L2; the waves' sums meet in LDS and are added in order.  One launch, no
-// workspace.  e4m3 is converted to bf16 fragments for every output type (the
-// conversion hides behind the loads).
-template <int NB, int MT, int W, bool F8>
-__global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w, int I, int J, int K, Epilogue ep) {
-    constexpr int U = MT == 1 ? 8 : 4;          // slabs in flight
-    constexpr int CH = F8 ? 16 : 8, SLAB = 4 * CH;  // values of k per lane and per slab
-    constexpr int ES = F8 ? 1 : 2;
-    constexpr int LDR = 16 * NB + 4;            // floats per row of a wave's sums
-    __shared__ __attribute__((aligned(16))) float sums[W][16 * MT][LDR];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int j0 = blockIdx.x * 16 * NB;
-    const long row = (long)K * ES;
-    const char *wp[NB], *xp[MT];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) wp[n] = w + (long)min(j0 + 16 * n + r, J - 1) * row;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) xp[m] = x + (long)min(16 * m + r, I - 1) * row;
-    // what the epilogue's threads will need
-    constexpr int PIECES = 2 * NB * 16 * MT;
-    const int pi = threadIdx.x / (2 * NB), pj = j0 + 8 * (threadIdx.x % (2 * NB));
-    const bool mine = threadIdx.x < PIECES && pi < I && pj < J, full = pj + 8 <= J;
-    Epilogue::Cols ec;
-    Epilogue::Row er;
-    if (PIECES <= W * 64 && mine && full) {
-        ec = ep.cols(pj, J);
-        er = ep.row(pi, pj);
-    }
-    f32x4 acc[NB][MT];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = zero4();
-    const int slabs = (K + SLAB - 1) / SLAB, per = (slabs + W - 1) / W;
-    const int s0 = wave * per, s1 = min(s0 + per, slabs);
-    for (int s = s0; s < s1; s += U) {
-        u32x4 fw[U][NB], fx[U][MT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (s + u) * SLAB + CH * g;
-            const bool in = s + u < s1 && k < K;
-            const long o = in ? (long)k * ES : 0;  // out of range: the row's start, not used
-#pragma unroll
-            for (int n = 0; n < NB; ++n) fw[u][n] = *(const u32x4 *)(wp[n] + o);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) fx[u][m] = *(const u32x4 *)(xp[m] + o);
-            if (!in) {  // both zero: an infinity times zero would not be
-#pragma unroll
-                for (int n = 0; n < NB; ++n) fw[u][n] = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int m = 0; m < MT; ++m) fx[u][m] = u32x4{0, 0, 0, 0};
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if constexpr (F8) {
-                u32x4 bx[MT][2];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) f8_to_bf16(bx[m], fx[u][m]);
-#pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    u32x4 bw[2];
-                    f8_to_bf16(bw, fw[u][n]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        acc[n][m] = mma_bf16_raw(acc[n][m], bw[0], bx[m][0]);
-                        acc[n][m] = mma_bf16_raw(acc[n][m], bw[1], bx[m][1]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) acc[n][m] = mma_bf16_raw(acc[n][m], fw[u][n], fx[u][m]);
-            }
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) *(f32x4 *)&sums[wave][16 * m + r][16 * n + 4 * g] = acc[n][m];
-    __syncthreads();
-    for (int q = threadIdx.x; q < PIECES; q += W * 64) {
-        const int i = q / (2 * NB), c = 8 * (q % (2 * NB)), j = j0 + c;
-        if (i >= I || j >= J) continue;
-        f32x8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = 0; p < W; ++p) {
-            const f32x4 lo = *(const f32x4 *)&sums[p][i][c], hi = *(const f32x4 *)&sums[p][i][c + 4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] += lo[e];
-                v[4 + e] += hi[e];
-            }
-        }
-        if (PIECES <= W * 64 && full) ep.whole(v, ec, er, i, j);
-        else ep.any(v, i, j, J);
-    }
-}
 
 // dz = dy act'(z) in `planes` bf16 planes (rounded; what is left of it; what
 // is left of that) of Jp columns, Jp a multiple of 8, zero past J; and the
@@ -662,7 +564,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
     const int i0 = blockIdx.y * rows, i1 = min(i0 + rows, I);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (j < Jp) {
-#pragma unroll 2
+#pragma unroll 4
         for (int i = i0 + wave; i < i1; i += 4) {
             float d[8];
             load_piece(d, dy + (long)i * J, j, J);
@@ -704,40 +606,66 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
 constexpr int kCUs = 256;
 
 // How a product of I x J over `slabs` slabs is cut: a tile size and a number
-// of splits of k.  With fewer tiles than compute units the sum is split so
-// that they fill the card once, as long as a split keeps 4 slabs.
+// of splits of k, the pair with the least estimated time.  The estimate is a
+// fit to measured launches (bf16 and e4m3, all operand orders, 1 to 2600
+// workgroups): 4 us a launch; a slab of the 128-tile takes 0.42 to 0.52 us
+// with at most one workgroup in each compute unit (four buffers, 2.5 us more
+// to start), 0.94 with two (two buffers), in between proportionally; a slab of
+// the 256-tile 1.2 us alone on the card to 1.55 with all compute units at
+// work; splits cost a second launch of 3 us and 8 bytes of partial sum per
+// output and split at 7 TB/s (they come back from the caches).  Four buffers
+// against two at 1024 x 4096 x 4096: 38.9 and 47.3 us.
 struct MmPlan {
     int tile, splits, per_split;
+    bool deep;  // one workgroup per compute unit, four buffers (128-tile)
 };
 
+static double mm_round_us(int tile, long n, int per) {  // n workgroups, at most one round
+    if (tile == 256) return per * (1.2 + 0.35 * n / kCUs);
+    return n <= kCUs ? 2.5 + per * (0.42 + 0.1 * n / kCUs) : per * (0.62 + 0.32 * (n - kCUs) / kCUs);
+}
+
 static MmPlan mm_plan(int I, int J, int slabs) {
-    MmPlan p;
-    const long big = (long)((I + 255) / 256) * ((J + 255) / 256);
-    p.tile = big >= kCUs ? 256 : 128;
-    const long tiles = (long)((I + p.tile - 1) / p.tile) * ((J + p.tile - 1) / p.tile);
-    int s = 1;
-    const long fill = 2 * kCUs;  // two workgroups of the small tile share a compute unit
-    if (p.tile == 128 && tiles * 2 <= fill) s = (int)(fill / tiles);
-    if (s > slabs / 4) s = slabs / 4;
-    if (s > 32) s = 32;
-    if (s < 1) s = 1;
-    p.per_split = (slabs + s - 1) / s;
-    p.splits = (slabs + p.per_split - 1) / p.per_split;
-    return p;
+    MmPlan best{};
+    double least = 1e30;
+    for (const int tile : {256, 128}) {
+        const long tiles = (long)((I + tile - 1) / tile) * ((J + tile - 1) / tile);
+        const long at_once = tile == 256 ? kCUs : 2 * kCUs;
+        for (int s = 1; s <= 32 && s * 2 <= (slabs > 2 ? slabs : 2); ++s) {
+            const int per = (slabs + s - 1) / s;
+            if ((slabs + per - 1) / per != s) continue;  // the same cut as a smaller s
+            const long n = tiles * s;
+            double us = 4.0 + (double)(n / at_once) * (mm_round_us(tile, at_once, per) + 2.0);
+            if (n % at_once) us += mm_round_us(tile, n % at_once, per);
+            if (s > 1) us += 3.0 + 8.0 * s * I * J / 7e6;
+            if (us < least) {
+                least = us;
+                best = MmPlan{tile, s, per, tile == 128 && n <= kCUs};
+            }
+        }
+    }
+    return best;
 }
 
 static size_t mm_part_bytes(const MmPlan &p, int I, int J) {
     return p.splits > 1 ? (size_t)p.splits * I * J * sizeof(float) : 0;
 }
 
-// The few-rows kernel takes up to kMvRows rows.
-constexpr int kMvRows = 64;
+// What the kernel for few rows or columns takes.  More columns are faster in
+// tiles (32768 x 64 x 4096: 54 us there, 68 here; x 8 x 1024: 18.2 and 16.3).
+constexpr int kFewRows = 64, kFewCols = 16;
+static bool mv_takes(int M, int N) { return M <= kFewRows || N <= kFewCols; }
 
 template <bool F8>
 static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, const Epilogue &ep, hipStream_t st) {
 #define GDN_MV(NBv, MTv, Wv, RBv)                                                                                  \
-    hipLaunchKernelGGL((mv_kernel<NBv, MTv, Wv, RBv, F8>), dim3((unsigned)((N + 16 * NBv - 1) / (16 * NBv))),      \
+    hipLaunchKernelGGL((mv_kernel<NBv, MTv, Wv, RBv, F8>),                                                         \
+                       dim3((unsigned)((N + 16 * NBv - 1) / (16 * NBv)), (unsigned)((M + 16 * MTv - 1) / (16 * MTv))), \
                        dim3(Wv * 64), 0, st, (const char *)x, (const char *)w, M, N, K, ep)
+    if (M > kFewRows) {  // few columns
+        GDN_MV(1, 2, 8, 256);
+        return hipGetLastError();
+    }
     // Up to 512 workgroups of 16 columns run in one or two rounds; more columns
     // go 32 to a workgroup, which reads x half as often (17 x 16384 x 1024 in
     // bf16: 8.8 against 13.5 us; 17 x 4096 x 4096: 10.2 against 15.9 the other
@@ -771,9 +699,11 @@ static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t 
     const dim3 grid((unsigned)(a.ti * a.tj), (unsigned)p.splits);
     float *pp = p.splits > 1 ? part : nullptr;
     if (p.tile == 256)
-        hipLaunchKernelGGL((mm_kernel<256, 256, 4, 2, TV, TU, MODE>), grid, dim3(512), 0, st, a, ep, pp);
+        hipLaunchKernelGGL((mm_kernel<256, 256, 4, 2, 2, TV, TU, MODE>), grid, dim3(512), 0, st, a, ep, pp);
+    else if (p.deep)
+        hipLaunchKernelGGL((mm_kernel<128, 128, 2, 2, 4, TV, TU, MODE>), grid, dim3(256), 0, st, a, ep, pp);
     else
-        hipLaunchKernelGGL((mm_kernel<128, 128, 2, 2, TV, TU, MODE>), grid, dim3(256), 0, st, a, ep, pp);
+        hipLaunchKernelGGL((mm_kernel<128, 128, 2, 2, 2, TV, TU, MODE>), grid, dim3(256), 0, st, a, ep, pp);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     const long pieces = (long)a.I * ((a.J + 7) / 8);
@@ -786,7 +716,7 @@ static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t 
 static int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
 
 size_t linear_ws_bytes(int M, int N, int K, bool f8) {
-    if (M <= kMvRows) return 0;
+    if (mv_takes(M, N)) return 0;
     return mm_part_bytes(mm_plan(M, N, slabs_of(K, f8)), M, N);
 }
 
@@ -799,17 +729,17 @@ hipError_t launch_linear(const void *x, const void *w, const float *xs, const fl
     a.ldv = a.ldu = K * es;
     a.I = M; a.J = N; a.K = K; a.parts = 1;
     const Epilogue ep{xs, ws, bias, residual, y, (uint16_t *)z, N, act, y_f32};
-    if (M <= kMvRows)
+    if (mv_takes(M, N))
         return f8 ? mv_run<true>(x, w, M, N, K, ep, st) : mv_run<false>(x, w, M, N, K, ep, st);
     if (!f8) return mm_run<false, false, MM_BF16>(a, ep, part, st);
     return y_f32 ? mm_run<false, false, MM_F8_F32>(a, ep, part, st) : mm_run<false, false, MM_F8>(a, ep, part, st);
 }
 
-// Rows of dz per workgroup of dz_kernel: about 512 workgroups, whole groups of
-// four rows.
+// Rows of dz per workgroup of dz_kernel: about 2048 workgroups, whole groups of
+// four rows for each of its waves.
 static int dz_rows(int M, int N) {
     const int cols = (N + 511) / 512;
-    const int want = (512 + cols - 1) / cols;
+    const int want = (2048 + cols - 1) / cols;
     int rows = (M + want - 1) / want;
     return (rows + 15) / 16 * 16;
 }

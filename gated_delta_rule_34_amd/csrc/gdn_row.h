@@ -96,6 +96,13 @@ __device__ __forceinline__ void store8v(float *p, const f32x8 &v) {
     *(f32x4_a4 *)p = f32x4_a4{v[0], v[1], v[2], v[3]};
     *(f32x4_a4 *)(p + 4) = f32x4_a4{v[4], v[5], v[6], v[7]};
 }
+// Non-temporal: for what this pass and the next one do not read.
+__device__ __forceinline__ void store8nt(uint16_t *p, const f32x8 &v) {
+    u32x4_a2 u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = pack2_bf16(v[2 * e], v[2 * e + 1]);
+    __builtin_nontemporal_store(u, (u32x4_a2 *)p);
+}
 template <class T>
 __device__ __forceinline__ f32x8 load8v(const T *p, int c, int D) {
     if (c + 8 <= D) return load8v(p + c);
