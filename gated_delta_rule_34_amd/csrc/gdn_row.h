@@ -125,6 +125,57 @@ __device__ __forceinline__ void store8v(T *p, const f32x8 &v, int c, int D) {
         if (c + e < D) store_elem(p + c + e, v[e]);
 }
 
+// Eight columns as they lie in memory (zero past D), for loads that are
+// issued long before their values are used.
+struct Raw16 {
+    u32x4 a;
+};
+struct Raw32 {
+    u32x4 a, b;
+};
+template <class T> struct RawOf;
+template <> struct RawOf<uint16_t> { using type = Raw16; };
+template <> struct RawOf<float> { using type = Raw32; };
+
+__device__ __forceinline__ Raw16 load_raw(const uint16_t *p, int c, int D) {
+    Raw16 o;
+    if (c + 8 <= D) {
+        o.a = *(const u32x4_a2 *)(p + c);
+    } else {
+        uint32_t t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = c + e < D ? p[c + e] : 0;
+        o.a = u32x4{t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16};
+    }
+    return o;
+}
+__device__ __forceinline__ Raw32 load_raw(const float *p, int c, int D) {
+    Raw32 o;
+    const uint32_t *u = (const uint32_t *)p;
+    typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (c + 8 <= D) {
+        o.a = *(const u32x4_a4 *)(u + c);
+        o.b = *(const u32x4_a4 *)(u + c + 4);
+    } else {
+        uint32_t t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = c + e < D ? u[c + e] : 0;
+        o.a = u32x4{t[0], t[1], t[2], t[3]};
+        o.b = u32x4{t[4], t[5], t[6], t[7]};
+    }
+    return o;
+}
+__device__ __forceinline__ f32x8 raw_f32(const Raw16 &r) { return bf16x8_to_f32(r.a); }
+__device__ __forceinline__ f32x8 raw_f32(const Raw32 &r) {
+    f32x8 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = __uint_as_float(r.a[e]);
+        v[4 + e] = __uint_as_float(r.b[e]);
+    }
+    return v;
+}
+
 // v / scale for one row: a reciprocal and one correction step, which gives the
 // correctly rounded quotient that a division would (codes are compared with
 // it, and quotients of bf16 values fall on e4m3's midpoints often); scales

@@ -8,7 +8,7 @@ Tolerances.  The kernels compute in fp32 and round each output once.
     partial sums, all positive, so the mean is within 54 * 2^-24 of its value
     relatively and s within half of that; u, s and the two products add four
     roundings: (27 + 4) 2^-24 < 2^-19.  fp32 bar 2^-18; bf16 bar 2^-8 + 2^-16.
-  - 8 bits: scale within 2^-18 relatively (its y's error and one division);
+  - 8 bits: scale within 2^-18 relatively (its y's error, a product and its constant's rounding);
     a code stands for its y within half a step, 2^-4 |y| or 2^-10 of the scale
     below the normal range, plus the 2^-17 by which y / scale may be off.
   - dx = s (w dy - xhat m) + dr with m a mean of 64-term thread sums: absolute
@@ -85,10 +85,10 @@ def test_norm_without_residual_and_quantiser(D, xd):
 
 def test_quantiser_rounds_as_a_division_does():
     """x / scale in fp32, rounded to nearest even: the codes of torch's division and conversion, ties included
-    (quotients of bf16 values fall on midpoints)."""
+    (quotients of bf16 values fall on midpoints).  The scale is max|x| times the fp32 number nearest to 1 / 448."""
     x = _t(np.random.default_rng(7), (64, 1024), BF)
     q, scale = gdn.gdn_quantize_rows(x)
-    s = x.float().abs().amax(dim=1) / torch.tensor(448.0, device="cuda")
+    s = x.float().abs().amax(dim=1) * (torch.ones(1, device="cuda") / torch.full((1,), 448.0, device="cuda"))
     assert torch.equal(scale, s)
     ref = (x.float() / s[:, None]).to(F8)
     assert torch.equal(q.view(torch.uint8), ref.view(torch.uint8))
