@@ -188,11 +188,12 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
     SV sv;
     SU su;
     constexpr int ES = F8 ? 1 : 2;
-    sv.init(a.V, a.ldv, i0, a.I - i0, a.K, lane, wave);
-    su.init(a.U, a.ldu, j0, a.J - j0, a.K, lane, wave);
     const int per = (a.K + SLAB - 1) / SLAB;       // slabs of one plane
     const int lastb = (a.K - (per - 1) * SLAB) * ES;  // k bytes of its last slab
     const int s0 = blockIdx.y * a.per_split, s1 = min(s0 + a.per_split, a.slabs);
+    const int p0 = s0 / per;
+    sv.init(a.V, a.ldv, i0, a.I - i0, a.K, a.part_stride, per, p0, s0 - p0 * per, lane, wave);
+    su.init(a.U, a.ldu, j0, a.J - j0, a.K, 0, per, p0, s0 - p0 * per, lane, wave);
     lds_cchar *lds = (lds_cchar *)smem;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
@@ -202,30 +203,42 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
 #pragma unroll
         for (int y = 0; y < NI; ++y) acc[x][y] = zero4();
 
-    // Slab loads: begin() takes the next slab's descriptors, piece() issues its
-    // n-th instruction of V, then of U, into buffer buf.
+    // Slab loads: piece() issues the n-th instruction of the slab that is due,
+    // V's first, into buffer buf; move() goes on to the next slab, in three
+    // steps that the loop spreads out.
     constexpr int LV = SV::kLoads, LU = SU::kLoads;
-    int p = s0 / per, s = s0 - p * per, next = s0;  // plane and slab of the next load
-    i32x4 rv, ru;
+    int s = s0 - p0 * per, next = s0;
+    bool last;
     int left;
-    auto begin = [&] {
-        const bool last = s == per - 1, live = next < s1;
-        rv = sv.slab(p * a.part_stride, s, last, live);
-        ru = su.slab(0, s, last, live);
+    auto bound = [&] {
+        last = s == per - 1;
         left = last ? lastb : 128;
-        ++next;
-        p += last;
-        s = last ? 0 : s + 1;
+        sv.bound(last, next < s1);
+        su.bound(last, next < s1);
+    };
+    auto move = [&](int step) {
+        if (step == 0) sv.advance(last);
+        if (step == 1) su.advance(last);
+        if (step == 2) {
+            s = last ? 0 : s + 1;
+            ++next;
+            bound();
+        }
     };
     auto piece = [&](int buf, int n) {
-        if (n < LV) sv.load(rv, lds0 + buf * BUF, n, left, wave);
-        else su.load(ru, lds0 + buf * BUF + SV::kBytes, n - LV, left, wave);
+        if (n < LV) sv.load(lds0 + buf * BUF, n, left, wave);
+        else su.load(lds0 + buf * BUF + SV::kBytes, n - LV, left, wave);
     };
     auto load = [&](int buf) {
-        begin();
 #pragma unroll
         for (int n = 0; n < LV + LU; ++n) piece(buf, n);
     };
+    auto move_on = [&] {
+        move(0);
+        move(1);
+        move(2);
+    };
+    bound();
     const int wi = (wave % WI) * NI * 16, wj = (wave / WI) * NJ * 16;
     if constexpr (MODE == MM_BF16) {
         // Fragments are read half a slab ahead of their products, in two
@@ -235,66 +248,144 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
         // Past the end the loads write zeros and the reads are not used,
         // which keeps the loop free of branches.
         u32x4 fv[2][NI], fu[2][NJ];
-        auto read = [&](auto set, int buf, int x) {  // x-th share of a set's reads
+        // n-th read of a set: the V fragments, which the first products all
+        // need, then those of U
+        auto read = [&](auto set, int buf, int n) {
             constexpr int h = decltype(set)::value;
             lds_cchar *iv = lds + buf * BUF, *iu = iv + SV::kBytes;
-            if (x < NI) fv[h][x] = mm_frag<BI, TV>(iv, wi + 16 * x, h, lane);
-            fu[h][x] = mm_frag<BJ, TU>(iu, wj + 16 * x, h, lane);
+            if (n < NI) fv[h][n] = mm_frag<BI, TV>(iv, wi + 16 * n, h, lane);
+            else fu[h][n - NI] = mm_frag<BJ, TU>(iu, wj + 16 * (n - NI), h, lane);
         };
-        auto mul = [&](auto set, int x) {
+        constexpr int R = NI + NJ, L = LV + LU, MM = NI * NJ;
+        // m-th product of a half, and nothing moved across it
+        auto mul = [&](auto set, int m) {
             constexpr int h = decltype(set)::value;
-            if (W == 8) __builtin_amdgcn_s_setprio(1);  // before the other wave's reads and loads: 2 %
-#pragma unroll
-            for (int y = 0; y < NI; ++y) acc[x][y] = mma_bf16_raw(acc[x][y], fu[h][x], fv[h][y]);
-            if (W == 8) __builtin_amdgcn_s_setprio(0);
+            const int x = m / NI, y = m % NI;
+            acc[x][y] = mma_bf16_raw(acc[x][y], fu[h][x], fv[h][y]);
+            __builtin_amdgcn_sched_barrier(0);
         };
-        static_assert(NI <= NJ, "shares");
         constexpr std::integral_constant<int, 0> h0;
         constexpr std::integral_constant<int, 1> h1;
         if (s0 < s1) {
 #pragma unroll
-            for (int n = 0; n < NBUF; ++n) load(n);
+            for (int n = 0; n < NBUF; ++n) {
+                if (n > 0) move_on();
+                load(n);
+            }
             mm_wait<(NBUF - 1) * (LV + LU)>();
             __builtin_amdgcn_s_barrier();
             mm_fence();
 #pragma unroll
-            for (int x = 0; x < NJ; ++x) read(h0, 0, x);
+            for (int n = 0; n < R; ++n) read(h0, 0, n);
         }
         int buf = 0;
         for (int t = s0; t < s1; ++t) {
-#pragma unroll
-            for (int x = 0; x < NJ; ++x) {
-                // (the first products go first: the wait for their operands,
-                // read before the loop's jump, is for all reads)
-                __builtin_amdgcn_sched_barrier(0);
-                if (x == 0) mul(h0, x);
-                __builtin_amdgcn_sched_barrier(0);
-                read(h1, buf, x);
-                __builtin_amdgcn_sched_barrier(0);
-                if (x > 0) mul(h0, x);
-            }
+            // About one read, or one slab load, after each product: they issue
+            // while the matrix cores are busy with it (in groups between
+            // groups of products, 1380 against 1430 TFLOP/s at 8192^3).  The
+            // last ones leave a few products before the half ends.
+            constexpr int E0 = MM * 6 / 8, E1 = MM * 7 / 8, OPS = R + L;
             __builtin_amdgcn_sched_barrier(0);
-            begin();
-            mm_wait<(NBUF - 2) * (LV + LU)>();
+#pragma unroll
+            for (int m = 0; m < MM; ++m) {
+                mul(h0, m);
+#pragma unroll
+                for (int n = m * R / E0; n < (m + 1) * R / E0 && n < R; ++n) read(h1, buf, n);
+                if (m == MM / 4) move(0);
+                if (m == MM / 2) move(1);
+                if (m == MM * 3 / 4) move(2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            mm_wait<(NBUF - 2) * L>();
             __builtin_amdgcn_s_barrier();
             mm_fence();
             const int after = buf + 1 < NBUF ? buf + 1 : 0;
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int x = 0; x < NJ; ++x) {
-                __builtin_amdgcn_sched_barrier(0);
-                read(h0, after, x);
+            for (int m = 0; m < MM; ++m) {
+                mul(h1, m);
 #pragma unroll
-                for (int n = x * (LV + LU) / NJ; n < (x + 1) * (LV + LU) / NJ; ++n) piece(buf, n);
+                for (int k = m * OPS / E1; k < (m + 1) * OPS / E1 && k < OPS; ++k) {
+                    // of OPS turns, L go to loads, evenly, the first one first
+                    const int before = (k * L + OPS - 1) / OPS, upto = ((k + 1) * L + OPS - 1) / OPS;
+                    if (upto > before) piece(buf, before);
+                    else read(h0, after, k - before);
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                mul(h1, x);
             }
             buf = after;
         }
         mm_wait<0>();  // the loads past the end have written before LDS is used again
+    } else if constexpr (MODE == MM_F8) {
+        // The same with whole-slab fragments: the products of the first half
+        // of the U fragments, then those of the second.  Every wave holds the
+        // second half's in registers when it comes to the middle; from there
+        // on the next slab's first half is read, and each V fragment as soon
+        // as its last product of this slab is under way.
+        constexpr int H = NJ / 2, MM = NI * H, L = LV + LU;
+        i32x8 fv[NI], fa[H], fb[H];
+        auto pair_v = [&](int buf, int y) {
+            lds_cchar *iv = lds + buf * BUF;
+            return mm_pair(mm_frag<BI, TV>(iv, wi + 16 * y, 0, lane), mm_frag<BI, TV>(iv, wi + 16 * y, 1, lane));
+        };
+        auto pair_u = [&](int buf, int x) {
+            lds_cchar *iu = lds + buf * BUF + SV::kBytes;
+            return mm_pair(mm_frag<BJ, TU>(iu, wj + 16 * x, 0, lane), mm_frag<BJ, TU>(iu, wj + 16 * x, 1, lane));
+        };
+        if (s0 < s1) {
+#pragma unroll
+            for (int n = 0; n < NBUF; ++n) {
+                if (n > 0) move_on();
+                load(n);
+            }
+            mm_wait<(NBUF - 1) * L>();
+            __builtin_amdgcn_s_barrier();
+            mm_fence();
+#pragma unroll
+            for (int y = 0; y < NI; ++y) fv[y] = pair_v(0, y);
+#pragma unroll
+            for (int x = 0; x < H; ++x) fa[x] = pair_u(0, x);
+        }
+        int buf = 0;
+        for (int t = s0; t < s1; ++t) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < MM; ++m) {
+                const int y = m / H, x = m % H;
+                acc[x][y] = mma_f8_slab(acc[x][y], fa[x], fv[y]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (m % 2 == 0 && m / 2 < H) fb[m / 2] = pair_u(buf, H + m / 2);
+                if (m == MM / 4) move(0);
+                if (m == MM / 2) move(1);
+                if (m == MM * 3 / 4) move(2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            mm_wait<(NBUF - 2) * L>();
+            __builtin_amdgcn_s_barrier();
+            mm_fence();
+            const int after = buf + 1 < NBUF ? buf + 1 : 0;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < MM; ++m) {
+                const int y = m / H, x = m % H;
+                acc[H + x][y] = mma_f8_slab(acc[H + x][y], fb[x], fv[y]);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = m * L / MM; n < (m + 1) * L / MM; ++n) piece(buf, n);
+                if (m % 2 == 1 && m / 2 < H) fa[m / 2] = pair_u(after, m / 2);
+                if (x == H - 1) fv[y] = pair_v(after, y);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            buf = after;
+        }
+        mm_wait<0>();
     } else {
         if (s0 < s1) {
 #pragma unroll
-            for (int n = 0; n < NBUF - 1; ++n) load(n);
+            for (int n = 0; n < NBUF - 1; ++n) {
+                load(n);
+                move_on();
+            }
         }
         int buf = 0;
         for (int t = s0; t < s1; ++t) {
@@ -304,35 +395,21 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
             __builtin_amdgcn_s_barrier();
             mm_fence();
             load(buf > 0 ? buf - 1 : NBUF - 1);
+            move_on();
             lds_cchar *iv = lds + buf * BUF, *iu = iv + SV::kBytes;
-            if constexpr (MODE == MM_F8) {
-                i32x8 fv[NI];
 #pragma unroll
-                for (int y = 0; y < NI; ++y)
-                    fv[y] = mm_pair(mm_frag<BI, TV>(iv, wi + 16 * y, 0, lane), mm_frag<BI, TV>(iv, wi + 16 * y, 1, lane));
+            for (int h = 0; h < 2; ++h) {
+                u32x4 fv[NI][2];
+#pragma unroll
+                for (int y = 0; y < NI; ++y) f8_to_bf16(fv[y], mm_frag<BI, TV>(iv, wi + 16 * y, h, lane));
 #pragma unroll
                 for (int x = 0; x < NJ; ++x) {
-                    const i32x8 fu =
-                        mm_pair(mm_frag<BJ, TU>(iu, wj + 16 * x, 0, lane), mm_frag<BJ, TU>(iu, wj + 16 * x, 1, lane));
+                    u32x4 fu[2];
+                    f8_to_bf16(fu, mm_frag<BJ, TU>(iu, wj + 16 * x, h, lane));
 #pragma unroll
-                    for (int y = 0; y < NI; ++y)
-                        acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fu, fv[y], acc[x][y], 0, 0, 0, 0, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    u32x4 fv[NI][2];
-#pragma unroll
-                    for (int y = 0; y < NI; ++y) f8_to_bf16(fv[y], mm_frag<BI, TV>(iv, wi + 16 * y, h, lane));
-#pragma unroll
-                    for (int x = 0; x < NJ; ++x) {
-                        u32x4 fu[2];
-                        f8_to_bf16(fu, mm_frag<BJ, TU>(iu, wj + 16 * x, h, lane));
-#pragma unroll
-                        for (int y = 0; y < NI; ++y) {
-                            acc[x][y] = mma_bf16_raw(acc[x][y], fu[0], fv[y][0]);
-                            acc[x][y] = mma_bf16_raw(acc[x][y], fu[1], fv[y][1]);
-                        }
+                    for (int y = 0; y < NI; ++y) {
+                        acc[x][y] = mma_bf16_raw(acc[x][y], fu[0], fv[y][0]);
+                        acc[x][y] = mma_bf16_raw(acc[x][y], fu[1], fv[y][1]);
                     }
                 }
             }

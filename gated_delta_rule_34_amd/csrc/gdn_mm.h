@@ -61,6 +61,10 @@ __device__ __forceinline__ i32x8 mm_pair(const u32x4 &lo, const u32x4 &hi) {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+__device__ __forceinline__ f32x4 mma_f8_slab(f32x4 acc, const i32x8 &a, const i32x8 &b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
+}
+
 // Waits until at most N of this wave's slab loads are in flight and its LDS
 // reads are done; nothing moves across.
 template <int N>
@@ -92,7 +96,8 @@ __device__ __forceinline__ i32x4 make_rsrc(const char *base, uint32_t bytes) {
 __device__ __forceinline__ int swz_row(int r) { return (r & 2) | ((r >> 1) & 4); }        // k contiguous
 __device__ __forceinline__ int swz_col(int k) { return (k & 3) | ((k >> 1) & 4); }        // k strided, pairs
 
-// Staging of one operand: R rows of the tile (R = BI or BJ).
+// Staging of one operand: R rows of the tile (R = BI or BJ), and the
+// descriptor of the slab that is loaded next.
 template <int R, int W, bool T>
 struct Stage {
     static constexpr int kBytes = R * 128;
@@ -100,14 +105,16 @@ struct Stage {
     static_assert(R % (8 * W) == 0, "whole instructions per wave");
     uint32_t off[kLoads];   // byte offsets of this lane's units, from the slab's base
     int chunk[kLoads];      // k contiguous: first k byte of the unit within the slab
-    const char *base;
-    long step;              // bytes from slab to slab
+    i32x4 rsrc;
+    long step, wrap;        // bytes to the next slab, and from a plane's last slab to the next plane's first
     uint32_t range, range_last;
 
-    // rows: valid rows from this tile's first on; K: bytes (k contiguous) or rows (k strided) of the sum
-    __device__ __forceinline__ void init(const char *p, long ld, int row0, int rows, int Kb, int lane, int wave) {
+    // rows: valid rows from this tile's first on; K: bytes (k contiguous) or rows (k strided) of the sum;
+    // plane, s: plane and slab of the first load, per slabs a plane, planes part bytes apart
+    __device__ __forceinline__ void init(const char *p, long ld, int row0, int rows, int Kb, long part, int per, int plane,
+                                         int s, int lane, int wave) {
         if (!T) {
-            base = p + (long)row0 * ld;
+            p += (long)row0 * ld;
             step = 128;
             range = range_last = (uint32_t)min(rows, R) * (uint32_t)ld;
 #pragma unroll
@@ -118,7 +125,7 @@ struct Stage {
             }
         } else {
             constexpr int UPR = R / 8;        // units per k row
-            base = p + (long)row0 * 2;
+            p += (long)row0 * 2;
             step = 64 * ld;
             range = (uint32_t)(64 * ld - (long)row0 * 2);
             const int left = Kb & 63;
@@ -130,17 +137,21 @@ struct Stage {
                 chunk[n] = 0;
             }
         }
+        wrap = part - (long)(per - 1) * step;
+        rsrc = make_rsrc(p + plane * part + s * step, 0);
     }
-    // Descriptor of slab s of the plane at `plane` bytes; a slab past the end
-    // (live false) has no range: its loads write zeros and read nothing.
-    __device__ __forceinline__ i32x4 slab(long plane, int s, bool last, bool live) const {
-        return make_rsrc(base + plane + (long)s * step, live ? (last ? range_last : range) : 0u);
+    // A slab past the end (live false) has no range: its loads write zeros and read nothing.
+    __device__ __forceinline__ void bound(bool last, bool live) { rsrc[2] = (int)(live ? (last ? range_last : range) : 0u); }
+    __device__ __forceinline__ void advance(bool last) {
+        const uint64_t at = ((uint64_t)(uint32_t)rsrc[1] << 32 | (uint32_t)rsrc[0]) + (uint64_t)(last ? wrap : step);
+        rsrc[0] = (int)(uint32_t)at;
+        rsrc[1] = (int)(uint32_t)(at >> 32);
     }
     // Instruction n of the slab into LDS at lds; left: bytes of k in the slab
     // (128 but for a k-contiguous operand's last one)
-    __device__ __forceinline__ void load(const i32x4 &rs, uint32_t lds, int n, int left, int wave) const {
+    __device__ __forceinline__ void load(uint32_t lds, int n, int left, int wave) const {
         const uint32_t o = T || chunk[n] < left ? off[n] : kOutOfRange;
-        lds_load(__builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave + W * n) * 1024), o, rs);
+        lds_load(__builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave + W * n) * 1024), o, rsrc);
     }
 };
 
