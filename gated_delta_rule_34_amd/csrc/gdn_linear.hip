@@ -124,26 +124,73 @@ struct Epilogue {
         }
         return v;
     }
-    // whole pieces (j + 8 <= J), with what cols() and row() fetched
-    __device__ __forceinline__ void whole(f32x8 v, const Cols &c, const Row &o, long i, int j) const {
-        v = before(v, c, o.a);
-        if (z) store8nt(z + i * ld + j, v);  // read again in the backward only
-        v = activate(v);
-        if (residual) {
-            if (y32) {
+    // N whole pieces (j + 8 <= J) in rows i, i + step, ..; with what cols()
+    // and row() fetched.  Each stage runs over all of them, so that the
+    // branches on what there is to do are taken once.
+    template <int N>
+    __device__ __forceinline__ void whole(f32x8 (&v)[N], const Cols &c, const Row (&o)[N], long i, int step, int j,
+                                          int I) const {
+        const long at = i * ld + j, hop = (long)step * ld;
+        const int n = i < I ? (int)((I - i + step - 1) / step) : 0;  // rows that are there
+        if (xs) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] += __uint_as_float(o.r0[e]);
-                    v[4 + e] += __uint_as_float(o.r1[e]);
-                }
-            } else {
-                const f32x8 t = bf16x8_to_f32(o.r0);
+            for (int q = 0; q < N; ++q)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += t[e];
-            }
+                for (int e = 0; e < 8; ++e) v[q][e] *= o[q].a * c.s[e];
         }
-        if (y32) store8v((float *)y + i * ld + j, v);
-        else store8v((uint16_t *)y + i * ld + j, v);
+        if (bias) {
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[q][e] += c.b[e];
+        }
+        if (z) {  // read again in the backward only
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (q < n) store8nt(z + at + q * hop, v[q]);
+        }
+        if (act == ACT_RELU) {
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[q][e] = act_fwd(ACT_RELU, v[q][e]);
+        } else if (act == ACT_SILU) {
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[q][e] = act_fwd(ACT_SILU, v[q][e]);
+        } else if (act == ACT_GELU) {
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[q][e] = act_fwd(ACT_GELU, v[q][e]);
+        }
+        if (y32) {
+            if (residual) {
+#pragma unroll
+                for (int q = 0; q < N; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[q][e] += __uint_as_float(o[q].r0[e]);
+                        v[q][4 + e] += __uint_as_float(o[q].r1[e]);
+                    }
+            }
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (q < n) store8v((float *)y + at + q * hop, v[q]);
+        } else {
+            if (residual) {
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    const f32x8 t = bf16x8_to_f32(o[q].r0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[q][e] += t[e];
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (q < n) store8v((uint16_t *)y + at + q * hop, v[q]);
+        }
     }
     // any piece that begins in the row
     __device__ __forceinline__ void any(f32x8 v, long i, int j, int J) const {
@@ -468,10 +515,10 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
             for (int q = 0; q < Q; ++q) o[q] = ep.row(min(ib + 16 * y + q * RPP, a.I - 1), j);
             put(y);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int i = ib + 16 * y + q * RPP;
-                const f32x8 v = get(q);
-                if (i < a.I) ep.whole(v, c, o[q], i, j);
+            for (int q = 0; q < Q; q += 2) {  // two at a time: four do not fit the registers
+                f32x8 v[2] = {get(q), get(q + 1)};
+                const Epilogue::Row o2[2] = {o[q], o[q + 1]};
+                ep.whole(v, c, o2, ib + 16 * y + q * RPP, RPP, j, a.I);
             }
         }
     } else {
@@ -621,8 +668,13 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
                 v[4 + e] += hi[e];
             }
         }
-        if (PIECES <= W * 64 && full) ep.whole(v, ec, er, i0 + i, j);
-        else ep.any(v, i0 + i, j, J);
+        if (PIECES <= W * 64 && full) {
+            f32x8 v1[1] = {v};
+            const Epilogue::Row er1[1] = {er};
+            ep.whole(v1, ec, er1, i0 + i, 1, j, I);
+        } else {
+            ep.any(v, i0 + i, j, J);
+        }
     }
 }
 
