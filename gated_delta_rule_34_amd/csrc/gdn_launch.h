@@ -163,7 +163,8 @@ hipError_t launch_linear(const void *x, const void *w, const float *xs, const fl
 struct LinearBwdPlan {
     int Np, planes, blocks;   // columns of a plane; planes; partial rows of dbias
     bool copy;                // dz is written to the workspace
-    size_t plane, sums_off, part_off, total;
+    bool pair, deep;          // both products in one launch; four buffers each
+    size_t plane, sums_off, part_off, part2_off, total;
 };
 LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, int act, bool dx, bool dw, bool dbias);
 hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,

@@ -215,10 +215,17 @@ struct Epilogue {
 // to bf16, which holds them exactly, as they leave LDS.
 enum { MM_BF16 = 0, MM_F8 = 1, MM_F8_F32 = 2 };
 
-// Grid: x = tiles, y = splits of k.  NBUF slabs in LDS.  part (nullable): fp32 partial sums
+// One tile of one split of k, with NBUF slabs in LDS.  part (nullable): fp32 partial sums
 // [split, I, J] instead of the epilogue.
+template <int BI, int BJ, int WI, int WJ, int NBUF>
+constexpr int mm_lds() {  // slabs, or the epilogue's image after them
+    constexpr int slabs = NBUF * (BI + BJ) * 128, image = WI * WJ * 16 * (BJ / WJ + 4) * 4;
+    return slabs > image ? slabs : image;
+}
+
 template <int BI, int BJ, int WI, int WJ, int NBUF, bool TV, bool TU, int MODE>
-__global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, float *part) {
+__device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilogue &ep, float *part, int tile,
+                                        int split) {
     constexpr bool F8 = MODE != MM_BF16;
     constexpr int W = WI * WJ, NI = BI / WI / 16, NJ = BJ / WJ / 16;  // 16-wide tiles per wave
     using SV = Stage<BI, W, TV>;
@@ -226,18 +233,16 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
     constexpr int SLAB = F8 ? 128 : 64;            // values of k per slab
     constexpr int BUF = SV::kBytes + SU::kBytes;
     constexpr int LDJ = BJ / WJ + 4;               // floats per row of the epilogue's image
-    constexpr int EPI = W * 16 * LDJ * 4;
-    __shared__ __attribute__((aligned(1024))) char smem[NBUF * BUF > EPI ? NBUF * BUF : EPI];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int bi, bj;
-    mm_tile(blockIdx.x, a.ti, a.tj, bi, bj);
+    mm_tile(tile, a.ti, a.tj, bi, bj);
     const int i0 = bi * BI, j0 = bj * BJ;
     SV sv;
     SU su;
     constexpr int ES = F8 ? 1 : 2;
     const int per = (a.K + SLAB - 1) / SLAB;       // slabs of one plane
     const int lastb = (a.K - (per - 1) * SLAB) * ES;  // k bytes of its last slab
-    const int s0 = blockIdx.y * a.per_split, s1 = min(s0 + a.per_split, a.slabs);
+    const int s0 = split * a.per_split, s1 = min(s0 + a.per_split, a.slabs);
     const int p0 = s0 / per;
     sv.init(a.V, a.ldv, i0, a.I - i0, a.K, a.part_stride, per, p0, s0 - p0 * per, lane, wave);
     su.init(a.U, a.ldu, j0, a.J - j0, a.K, 0, per, p0, s0 - p0 * per, lane, wave);
@@ -495,7 +500,7 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
         return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
     if (part) {
-        part += (long)blockIdx.y * a.I * a.J;
+        part += (long)split * a.I * a.J;
 #pragma unroll 1
         for (int y = 0; y < NI; ++y) {
             put(y);
@@ -533,6 +538,24 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
             }
         }
     }
+}
+
+// Grid: x = tiles, y = splits of k.
+template <int BI, int BJ, int WI, int WJ, int NBUF, bool TV, bool TU, int MODE>
+__global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, float *part) {
+    __shared__ __attribute__((aligned(1024))) char smem[mm_lds<BI, BJ, WI, WJ, NBUF>()];
+    mm_body<BI, BJ, WI, WJ, NBUF, TV, TU, MODE>(smem, a, ep, part, blockIdx.x, blockIdx.y);
+}
+
+// Both products of the backward in one launch, where neither fills the card:
+// workgroups 0 .. na - 1 are dx's tiles and splits, the others dw's.
+template <int NBUF>
+__global__ __launch_bounds__(256) void mm_pair_kernel(MmArgs a, Epilogue ea, float *pa, int na, MmArgs b, Epilogue eb,
+                                                      float *pb) {
+    __shared__ __attribute__((aligned(1024))) char smem[mm_lds<128, 128, 2, 2, NBUF>()];
+    const int g = blockIdx.x, ta = a.ti * a.tj, tb = b.ti * b.tj;
+    if (g < na) mm_body<128, 128, 2, 2, NBUF, false, true, MM_BF16>(smem, a, ea, pa, g % ta, g / ta);
+    else mm_body<128, 128, 2, 2, NBUF, true, true, MM_BF16>(smem, b, eb, pb, (g - na) % tb, (g - na) / tb);
 }
 
 // Adds the partial sums of the splits in order and applies the epilogue.
@@ -817,14 +840,30 @@ static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, cons
     return hipGetLastError();
 }
 
-template <bool TV, bool TU, int MODE>
-static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t st) {
-    const int slab = MODE == MM_BF16 ? 64 : 128;
-    a.slabs = a.parts * ((a.K + slab - 1) / slab);
+static int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
+
+// Fills in what the plan decides.
+static MmPlan mm_set(MmArgs &a, bool f8) {
+    a.slabs = a.parts * slabs_of(a.K, f8);
     const MmPlan p = mm_plan(a.I, a.J, a.slabs);
     a.per_split = p.per_split;
     a.ti = (a.I + p.tile - 1) / p.tile;
     a.tj = (a.J + p.tile - 1) / p.tile;
+    return p;
+}
+
+static hipError_t mm_join(const MmArgs &a, const MmPlan &p, const Epilogue &ep, const float *part, hipStream_t st) {
+    if (p.splits == 1) return hipSuccess;
+    const long pieces = (long)a.I * ((a.J + 7) / 8);
+    const long blocks = (pieces + 255) / 256;
+    hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, part, ep,
+                       p.splits, a.I, a.J);
+    return hipGetLastError();
+}
+
+template <bool TV, bool TU, int MODE>
+static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t st) {
+    const MmPlan p = mm_set(a, MODE != MM_BF16);
     const dim3 grid((unsigned)(a.ti * a.tj), (unsigned)p.splits);
     float *pp = p.splits > 1 ? part : nullptr;
     if (p.tile == 256)
@@ -833,16 +872,9 @@ static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t 
         hipLaunchKernelGGL((mm_kernel<128, 128, 2, 2, 4, TV, TU, MODE>), grid, dim3(256), 0, st, a, ep, pp);
     else
         hipLaunchKernelGGL((mm_kernel<128, 128, 2, 2, 2, TV, TU, MODE>), grid, dim3(256), 0, st, a, ep, pp);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    const long pieces = (long)a.I * ((a.J + 7) / 8);
-    const long blocks = (pieces + 255) / 256;
-    hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, part, ep,
-                       p.splits, a.I, a.J);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : mm_join(a, p, ep, part, st);
 }
-
-static int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
 
 size_t linear_ws_bytes(int M, int N, int K, bool f8) {
     if (mv_takes(M, N)) return 0;
@@ -887,13 +919,18 @@ LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, i
     p.blocks = (M + rows - 1) / rows;
     if (dbias) off += up((size_t)p.blocks * N * 4);
     p.part_off = off;
-    size_t part = 0;
-    if (dx) part = mm_part_bytes(mm_plan(M, K, p.planes * slabs_of(N, false)), M, K);
-    if (dw) {
-        const size_t b = mm_part_bytes(mm_plan(N, K, p.planes * slabs_of(M, false)), N, K);
-        if (b > part) part = b;
-    }
-    p.total = off + up(part);
+    MmPlan a{}, b{};
+    if (dx) a = mm_plan(M, K, p.planes * slabs_of(N, false));
+    if (dw) b = mm_plan(N, K, p.planes * slabs_of(M, false));
+    const size_t pa = dx ? up(mm_part_bytes(a, M, K)) : 0, pb = dw ? up(mm_part_bytes(b, N, K)) : 0;
+    // both products at once where they fit the card together
+    auto groups = [&](const MmPlan &m, int I) {
+        return (long)((I + m.tile - 1) / m.tile) * ((K + m.tile - 1) / m.tile) * m.splits;
+    };
+    p.pair = dx && dw && a.tile == 128 && b.tile == 128 && groups(a, M) + groups(b, N) <= 2 * kCUs;
+    p.deep = p.pair && groups(a, M) + groups(b, N) <= kCUs;
+    p.part2_off = p.part_off + (p.pair ? pa : 0);
+    p.total = p.pair ? p.part2_off + pb : off + (pa > pb ? pa : pb);
     return p;
 }
 
@@ -924,24 +961,34 @@ hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const
             if (e != hipSuccess) return e;
         }
     }
-    float *part = (float *)(ws + p.part_off);
-    if (dx) {  // V = dz [M, N] along n, U = W [N, K] with n as its rows
-        MmArgs a{};
-        a.V = (const char *)dz; a.ldv = (long)p.Np * 2; a.parts = p.planes; a.part_stride = (long)p.plane;
-        a.U = (const char *)w; a.ldu = (long)K * 2;
-        a.I = M; a.J = K; a.K = N;
-        const Epilogue ep{nullptr, nullptr, nullptr, nullptr, dx, nullptr, K, ACT_NONE, grad_f32};
-        e = mm_run<false, true, MM_BF16>(a, ep, part, st);
-        if (e != hipSuccess) return e;
+    float *pa = (float *)(ws + p.part_off), *pb = (float *)(ws + p.part2_off);
+    // dx: V = dz [M, N] along n, U = W [N, K] with n as its rows; dw: V = dz with m as its rows, U = x [M, K]
+    MmArgs a{}, b{};
+    a.V = b.V = (const char *)dz;
+    a.ldv = b.ldv = (long)p.Np * 2;
+    a.parts = b.parts = p.planes;
+    a.part_stride = b.part_stride = (long)p.plane;
+    a.U = (const char *)w;
+    b.U = (const char *)x;
+    a.ldu = b.ldu = (long)K * 2;
+    a.I = M; a.J = K; a.K = N;
+    b.I = N; b.J = K; b.K = M;
+    const Epilogue ea{nullptr, nullptr, nullptr, nullptr, dx, nullptr, K, ACT_NONE, grad_f32};
+    const Epilogue eb{nullptr, nullptr, nullptr, nullptr, dw, nullptr, K, ACT_NONE, grad_f32};
+    if (p.pair) {
+        const MmPlan qa = mm_set(a, false), qb = mm_set(b, false);
+        const int na = a.ti * a.tj * qa.splits, nb = b.ti * b.tj * qb.splits;
+        float *sa = qa.splits > 1 ? pa : nullptr, *sb = qb.splits > 1 ? pb : nullptr;
+        if (p.deep)
+            hipLaunchKernelGGL((mm_pair_kernel<4>), dim3((unsigned)(na + nb)), dim3(256), 0, st, a, ea, sa, na, b, eb, sb);
+        else
+            hipLaunchKernelGGL((mm_pair_kernel<2>), dim3((unsigned)(na + nb)), dim3(256), 0, st, a, ea, sa, na, b, eb, sb);
+        e = hipGetLastError();
+        if (e == hipSuccess) e = mm_join(a, qa, ea, pa, st);
+        return e != hipSuccess ? e : mm_join(b, qb, eb, pb, st);
     }
-    if (dw) {  // V = dz [M, N] with m as its rows, U = x [M, K]
-        MmArgs a{};
-        a.V = (const char *)dz; a.ldv = (long)p.Np * 2; a.parts = p.planes; a.part_stride = (long)p.plane;
-        a.U = (const char *)x; a.ldu = (long)K * 2;
-        a.I = N; a.J = K; a.K = M;
-        const Epilogue ep{nullptr, nullptr, nullptr, nullptr, dw, nullptr, K, ACT_NONE, grad_f32};
-        e = mm_run<true, true, MM_BF16>(a, ep, part, st);
-    }
+    if (dx) e = mm_run<false, true, MM_BF16>(a, ea, pa, st);
+    if (dw && e == hipSuccess) e = mm_run<true, true, MM_BF16>(b, eb, pb, st);
     return e;
 }
 
