@@ -760,6 +760,11 @@ def _act_code(act):
     return code
 
 
+def _multiple(K, of):
+    if K % of:
+        raise ValueError(f"K must be a multiple of {of}, got {K}")
+
+
 def gdn_linear_workspace(M, N, K, dtype_code):
     return int(load().gdn_linear_workspace(M, N, K, dtype_code))
 
@@ -788,6 +793,7 @@ def gdn_linear(x, weight, bias=None, residual=None, act="none", x_scale=None, w_
         raise ValueError("x_scale and w_scale belong to float8_e4m3fn operands")
     if bias is not None:
         _need(bias, "bias", (N,), f32, dev)
+    _multiple(K, 16 if dt == torch.float8_e4m3fn else 8)
     odt = torch.bfloat16 if out_dtype is None else out_dtype
     shape = lead + (N,)
     if residual is not None:
@@ -836,6 +842,7 @@ def gdn_linear_bwd(dy, x, weight, z=None, act="none", bias=False, grad_dtype=Non
         _need(z, "z", lead + (N,), bf, dev)
     elif act != "none":
         raise ValueError(f"act {act!r} needs z")
+    _multiple(K, 8)
     M = x.numel() // K if K else 0
     gdt = bf if grad_dtype is None else grad_dtype
     dx = torch.empty_like(x, dtype=gdt) if need_dx else None

@@ -682,7 +682,7 @@ gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long row
 // Sizes of a product the kernels index: 32-bit offsets within a tile of 256
 // rows, a grid of fewer than 2^32 threads.
 static bool mm_sizes_ok(int M, int N, int K) {
-    auto tiles = [](long long a, long long b) { return ((a + 255) / 256) * ((b + 255) / 256) < (1LL << 22); };
+    auto tiles = [](long long a, long long b) { return ((a + 255) / 256) * ((b + 255) / 256) < (1LL << 21); };
     return N <= (1 << 22) && K <= (1 << 22) && tiles(M, N) && tiles(M, K) && tiles(N, K);
 }
 

@@ -103,7 +103,7 @@ struct Epilogue {
     __device__ __forceinline__ f32x8 before(f32x8 v, const Cols &c, float a) const {
         if (xs) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= a * c.s[e];
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * a * c.s[e];
         }
         if (bias) {
 #pragma unroll
@@ -136,7 +136,7 @@ struct Epilogue {
 #pragma unroll
             for (int q = 0; q < N; ++q)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[q][e] *= o[q].a * c.s[e];
+                for (int e = 0; e < 8; ++e) v[q][e] = v[q][e] * o[q].a * c.s[e];
         }
         if (bias) {
 #pragma unroll
@@ -598,7 +598,8 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
     __shared__ __attribute__((aligned(1024))) char smem[W * (WB + XB) > SB ? W * (WB + XB) : SB];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int j0 = blockIdx.x * 16 * NB, i0 = blockIdx.y * 16 * MT;
+    const int tj = (J + 16 * NB - 1) / (16 * NB);
+    const int j0 = (int)(blockIdx.x % tj) * 16 * NB, i0 = (int)(blockIdx.x / tj) * 16 * MT;
     const int rows = min(16 * MT, I - i0);
     const uint32_t row = (uint32_t)K * ES;
     // what the epilogue's threads will need
@@ -806,13 +807,15 @@ static size_t mm_part_bytes(const MmPlan &p, int I, int J) {
 // What the kernel for few rows or columns takes.  More columns are faster in
 // tiles (32768 x 64 x 4096: 54 us there, 68 here; x 8 x 1024: 18.2 and 16.3).
 constexpr int kFewRows = 64, kFewCols = 16;
-static bool mv_takes(int M, int N) { return M <= kFewRows || N <= kFewCols; }
+static bool mv_takes(int M, int N) {
+    return M <= kFewRows || (N <= kFewCols && M < (1 << 27));  // a launch holds fewer than 2^32 threads
+}
 
 template <bool F8>
 static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, const Epilogue &ep, hipStream_t st) {
 #define GDN_MV(NBv, MTv, Wv, RBv)                                                                                  \
     hipLaunchKernelGGL((mv_kernel<NBv, MTv, Wv, RBv, F8>),                                                         \
-                       dim3((unsigned)((N + 16 * NBv - 1) / (16 * NBv)), (unsigned)((M + 16 * MTv - 1) / (16 * MTv))), \
+                       dim3((unsigned)((N + 16 * NBv - 1) / (16 * NBv)) * (unsigned)((M + 16 * MTv - 1) / (16 * MTv))), \
                        dim3(Wv * 64), 0, st, (const char *)x, (const char *)w, M, N, K, ep)
     if (M > kFewRows) {  // few columns
         GDN_MV(1, 2, 8, 256);

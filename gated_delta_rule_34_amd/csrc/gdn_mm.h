@@ -80,7 +80,7 @@ __device__ __forceinline__ void lds_load(uint32_t lds, uint32_t voff, i32x4 rsrc
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory");
+                 : "m0", "memory");
 }
 
 __device__ __forceinline__ i32x4 make_rsrc(const char *base, uint32_t bytes) {

@@ -449,7 +449,7 @@ typedef enum { GDN_ACT_NONE = 0, GDN_ACT_RELU = 1, GDN_ACT_SILU = 2, GDN_ACT_GEL
  * K with few tiles is summed in a fixed number of parts that depends on the
  * sizes alone (fp32 partial sums in the workspace, added in order).
  *   M, N >= 1, any value; K a multiple of 8 (bf16) or 16 (8 bits); N and K at
- *   most 2^22 and ceil(M / 256) * ceil(N / 256) below 2^22
+ *   most 2^22 and ceil(M / 256) * ceil(N / 256) below 2^21
  *   x, w and residual, y, z 16-byte aligned
  *   ws  gdn_linear_workspace() bytes, 256-byte aligned (may be NULL if 0)
  * Errors: GDN_ERR_INVALID_ARG (null required pointers, scales that do not

@@ -168,6 +168,8 @@ def test_linear_binding_refuses_wrong_tensors():
         gdn.gdn_linear(x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn))
     with pytest.raises(TypeError, match="residual"):
         gdn.gdn_linear(x, w, residual=torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="multiple of 8"):
+        gdn.gdn_linear(x[:, :12].contiguous(), w[:, :12].contiguous())
     with pytest.raises(ValueError, match="needs z"):
         gdn.gdn_linear_bwd(torch.zeros(4, 8), x, w, act="silu")
 

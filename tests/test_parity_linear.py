@@ -50,7 +50,7 @@ def _close(x, ref, bar, what):
 # one row, one column, one slab; each kernel's tile edge and both sides of it; sums split in parts; whole large tiles
 SHAPES = [(1, 1, 8), (1, 5, 64), (2, 64, 72), (3, 129, 1024), (15, 16, 520), (16, 4096, 64), (17, 255, 136), (31, 33, 4096),
           (33, 1000, 256), (64, 64, 8192), (65, 130, 64), (127, 128, 192), (128, 127, 128), (129, 257, 1024), (255, 300, 48),
-          (256, 256, 64), (257, 513, 1032), (1000, 8, 1024), (8, 1031, 1024), (640, 4104, 160), (4097, 4099, 56),
+          (256, 256, 64), (3000, 16, 264), (5000, 17, 64), (257, 513, 1032), (1000, 8, 1024), (8, 1031, 1024), (640, 4104, 160), (4097, 4099, 56),
           (4096, 4096, 128)]
 
 
@@ -195,6 +195,23 @@ def test_infinities_and_nan_stay_in_their_row_and_column():
     keep_i = [i for i in range(M) if i not in (7, 149)]
     assert torch.equal(y[keep_i][:, :139], clean[keep_i][:, :139])
     assert torch.isnan(y[7]).all() and torch.isnan(y[:, 139]).all() and not torch.isfinite(y[149]).any()
+
+
+@pytest.mark.parametrize("M,out", [(20, BF), (20, F32), (200, BF), (200, F32)])
+def test_infinities_and_nan_in_8_bits(M, out):
+    """A NaN code spoils its row (its column, in the weights) and nothing else; an infinite scale gives infinities."""
+    rng = np.random.default_rng(27)
+    N, K = 150, 208
+    x, w = _ints(rng, (M, K), 3, F32), _ints(rng, (N, K), 3, F32)
+    xs, ws = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    x[:, 0] = 1
+    clean = gdn.gdn_linear(x.to(F8), w.to(F8), x_scale=xs, w_scale=ws, out_dtype=out)[0]
+    x[7, 207], w[149, 100] = float("nan"), float("nan")
+    xs[11] = float("inf")
+    y = gdn.gdn_linear(x.to(F8), w.to(F8), x_scale=xs, w_scale=ws, out_dtype=out)[0]
+    keep = [i for i in range(M) if i not in (7, 11)]
+    assert torch.equal(y[keep][:, :149], clean[keep][:, :149])
+    assert torch.isnan(y[7]).all() and torch.isnan(y[:, 149]).all() and not torch.isfinite(y[11]).any()
 
 
 @pytest.mark.parametrize("M,N", [(5, 37), (130, 136), (600, 1100)])
