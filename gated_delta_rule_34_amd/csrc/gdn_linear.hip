@@ -76,7 +76,6 @@ struct Epilogue {
         f32x8 s, b;
     };
     struct Row {
-        float a;
         u32x4 r0, r1;  // residual: eight bf16, or eight fp32
     };
     __device__ __forceinline__ Cols cols(int j, int J) const {
@@ -85,18 +84,15 @@ struct Epilogue {
         if (bias) c.b = load8v(bias, j, J);
         return c;
     }
-    // only for j + 8 <= J
+    // the residual's piece, only for j + 8 <= J
     __device__ __forceinline__ Row row(long i, int j) const {
         Row o;
-        if (xs) o.a = xs[i];
-        if (residual) {
-            if (y32) {
-                const u32x4_a2 *p = (const u32x4_a2 *)((const float *)residual + i * ld + j);
-                o.r0 = p[0];
-                o.r1 = p[1];
-            } else {
-                o.r0 = *(const u32x4_a2 *)((const uint16_t *)residual + i * ld + j);
-            }
+        if (y32) {
+            const u32x4_a2 *p = (const u32x4_a2 *)((const float *)residual + i * ld + j);
+            o.r0 = p[0];
+            o.r1 = p[1];
+        } else {
+            o.r0 = *(const u32x4_a2 *)((const uint16_t *)residual + i * ld + j);
         }
         return o;
     }
@@ -124,19 +120,21 @@ struct Epilogue {
         }
         return v;
     }
-    // N whole pieces (j + 8 <= J) in rows i, i + step, ..; with what cols()
-    // and row() fetched.  Each stage runs over all of them, so that the
-    // branches on what there is to do are taken once.
-    template <int N>
+    // N whole pieces (j + 8 <= J) in rows i, i + step, .., x_scale applied
+    // already; with what cols() and, RES, row() fetched.  Each stage runs over
+    // all of them, so that the branches on what there is to do are taken
+    // once.  Nothing is loaded here: a wait for a load is a wait for every
+    // store before it.
+    template <bool XS, bool RES, int N>
     __device__ __forceinline__ void whole(f32x8 (&v)[N], const Cols &c, const Row (&o)[N], long i, int step, int j,
                                           int I) const {
         const long at = i * ld + j, hop = (long)step * ld;
         const int n = i < I ? (int)((I - i + step - 1) / step) : 0;  // rows that are there
-        if (xs) {
+        if (XS) {
 #pragma unroll
             for (int q = 0; q < N; ++q)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[q][e] = v[q][e] * o[q].a * c.s[e];
+                for (int e = 0; e < 8; ++e) v[q][e] *= c.s[e];
         }
         if (bias) {
 #pragma unroll
@@ -166,7 +164,7 @@ struct Epilogue {
                 for (int e = 0; e < 8; ++e) v[q][e] = act_fwd(ACT_GELU, v[q][e]);
         }
         if (y32) {
-            if (residual) {
+            if (RES) {
 #pragma unroll
                 for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -179,7 +177,7 @@ struct Epilogue {
             for (int q = 0; q < N; ++q)
                 if (q < n) store8v((float *)y + at + q * hop, v[q]);
         } else {
-            if (residual) {
+            if (RES) {
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
                     const f32x8 t = bf16x8_to_f32(o[q].r0);
@@ -219,7 +217,7 @@ enum { MM_BF16 = 0, MM_F8 = 1, MM_F8_F32 = 2 };
 // [split, I, J] instead of the epilogue.
 template <int BI, int BJ, int WI, int WJ, int NBUF>
 constexpr int mm_lds() {  // slabs, or the epilogue's image after them
-    constexpr int slabs = NBUF * (BI + BJ) * 128, image = WI * WJ * 16 * (BJ / WJ + 4) * 4;
+    constexpr int slabs = NBUF * (BI + BJ) * 128, image = WI * WJ * 16 * (BJ / WJ + 4) * 4 + WJ * BI * 4;
     return slabs > image ? slabs : image;
 }
 
@@ -476,6 +474,7 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
     // the rows add is fetched ahead of the products' way through LDS.
     __syncthreads();
     float *img = (float *)smem + wave * 16 * LDJ;
+    float *scales = (float *)smem + W * 16 * LDJ + wave * NI * 16;
     constexpr int LPR = NJ * 2, RPP = 64 / LPR, Q = 16 / RPP;  // lanes per row, rows per pass, passes
     const int r = lane & 15, g = lane >> 4, c8 = (lane % LPR) * 8, rr = lane / LPR;
     const int j = j0 + wj + c8, ib = i0 + wi + rr;
@@ -499,6 +498,28 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
         const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 4);
         return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
+    auto rows = [&](auto res, const Epilogue::Cols &c) {
+        constexpr bool RES = decltype(res)::value;
+#pragma unroll 1
+        for (int y = 0; y < NI; ++y) {
+            Epilogue::Row o[Q];
+            if (RES) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) o[q] = ep.row(min(ib + 16 * y + q * RPP, a.I - 1), j);
+            }
+            put(y);
+#pragma unroll
+            for (int q = 0; q < Q; q += 2) {  // two at a time: four do not fit the registers
+                f32x8 v[2] = {get(q), get(q + 1)};
+                if (F8) {
+                    v[0] *= scales[16 * y + q * RPP + rr];
+                    v[1] *= scales[16 * y + (q + 1) * RPP + rr];
+                }
+                const Epilogue::Row o2[2] = {o[q], o[q + 1]};
+                ep.whole<F8, RES>(v, c, o2, ib + 16 * y + q * RPP, RPP, j, a.I);
+            }
+        }
+    };
     if (part) {
         part += (long)split * a.I * a.J;
 #pragma unroll 1
@@ -512,20 +533,16 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
             }
         }
     } else if (j0 + BJ <= a.J) {
-        const Epilogue::Cols c = ep.cols(j, a.J);
-#pragma unroll 1
-        for (int y = 0; y < NI; ++y) {
-            Epilogue::Row o[Q];
+        // x_scale by way of LDS: loaded in the loop, it would wait for the
+        // stores there; applied to the accumulators, it would double them
+        if (F8) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) o[q] = ep.row(min(ib + 16 * y + q * RPP, a.I - 1), j);
-            put(y);
-#pragma unroll
-            for (int q = 0; q < Q; q += 2) {  // two at a time: four do not fit the registers
-                f32x8 v[2] = {get(q), get(q + 1)};
-                const Epilogue::Row o2[2] = {o[q], o[q + 1]};
-                ep.whole(v, c, o2, ib + 16 * y + q * RPP, RPP, j, a.I);
-            }
+            for (int k = 0; k < NI; ++k)
+                if (g == 0) scales[16 * k + r] = ep.xs[min(i0 + wi + 16 * k + r, a.I - 1)];
         }
+        const Epilogue::Cols c = ep.cols(j, a.J);
+        if (ep.residual) rows(std::true_type{}, c);
+        else rows(std::false_type{}, c);
     } else {
 #pragma unroll 1
         for (int y = 0; y < NI; ++y) {
@@ -607,9 +624,11 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
     const bool mine = threadIdx.x < PIECES && pi < rows && pj < J, full = pj + 8 <= J;
     Epilogue::Cols ec;
     Epilogue::Row er;
+    float ea = 1.f;
     if (PIECES <= W * 64 && mine && full) {
         ec = ep.cols(pj, J);
-        er = ep.row(i0 + pi, pj);
+        if (F8) ea = ep.xs[i0 + pi];
+        if (ep.residual) er = ep.row(i0 + pi, pj);
     }
     f32x4 acc[NB][MT];
 #pragma unroll
@@ -693,9 +712,10 @@ __global__ __launch_bounds__(W * 64) void mv_kernel(const char *x, const char *w
             }
         }
         if (PIECES <= W * 64 && full) {
-            f32x8 v1[1] = {v};
+            f32x8 v1[1] = {F8 ? v * ea : v};
             const Epilogue::Row er1[1] = {er};
-            ep.whole(v1, ec, er1, i0 + i, 1, j, I);
+            if (ep.residual) ep.whole<F8, true>(v1, ec, er1, i0 + i, 1, j, I);
+            else ep.whole<F8, false>(v1, ec, er1, i0 + i, 1, j, I);
         } else {
             ep.any(v, i0 + i, j, J);
         }

@@ -185,12 +185,12 @@ __device__ __forceinline__ u32x4 mm_frag(lds_cchar *img, int row0, int s, int la
 }
 
 // The tile (bi, bj) of workgroup b of n.  Workgroup b runs on XCD b % 8: each
-// XCD gets a contiguous run of tiles, walked in bands of 8 tile rows, so that
+// XCD gets a contiguous run of tiles, walked in bands of 4 tile rows, so that
 // the tiles an XCD works on at a time share their operand rows in its L2.
 __device__ __forceinline__ void mm_tile(int b, int ti, int tj, int &bi, int &bj) {
     const int n = ti * tj, q = n / 8, rem = n % 8, x = b % 8;
     const int id = x * q + min(x, rem) + b / 8;
-    constexpr int BAND = 8;
+    constexpr int BAND = 4;
     const int band = id / (BAND * tj), first = band * BAND, h = min(BAND, ti - first);
     const int in = id - band * BAND * tj;
     bi = first + in % h;
