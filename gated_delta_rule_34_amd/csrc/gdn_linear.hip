@@ -12,6 +12,8 @@
 
 namespace gdn {
 
+constexpr int kCUs = 256;  // compute units of the MI355X
+
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 
 __device__ __forceinline__ float sigmoid_fast(float z) {
@@ -71,6 +73,7 @@ struct Epilogue {
     long ld;        // columns of y, residual and z
     int act;
     bool y32;
+    bool past;      // y is larger than the L2 caches together: it leaves by non-temporal stores
     // What columns j .. j + 7 share over all rows, and what a row adds.
     struct Cols {
         f32x8 s, b;
@@ -175,7 +178,7 @@ struct Epilogue {
             }
 #pragma unroll
             for (int q = 0; q < N; ++q)
-                if (q < n) store8v((float *)y + at + q * hop, v[q]);
+                if (q < n) store8p((float *)y + at + q * hop, v[q], past);
         } else {
             if (RES) {
 #pragma unroll
@@ -187,7 +190,7 @@ struct Epilogue {
             }
 #pragma unroll
             for (int q = 0; q < N; ++q)
-                if (q < n) store8v((uint16_t *)y + at + q * hop, v[q]);
+                if (q < n) store8p((uint16_t *)y + at + q * hop, v[q], past);
         }
     }
     // any piece that begins in the row
@@ -231,6 +234,8 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
     constexpr int SLAB = F8 ? 128 : 64;            // values of k per slab
     constexpr int BUF = SV::kBytes + SU::kBytes;
     constexpr int LDJ = BJ / WJ + 4;               // floats per row of the epilogue's image
+    constexpr bool AHEAD = BI == 256 && !TV;       // see the epilogue
+    static_assert(!AHEAD || W * 16 * LDJ * 4 + WJ * BI * 4 + W * 256 <= mm_lds<BI, BJ, WI, WJ, NBUF>(), "room");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int bi, bj;
     mm_tile(tile, a.ti, a.tj, bi, bj);
@@ -475,6 +480,26 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
     __syncthreads();
     float *img = (float *)smem + wave * 16 * LDJ;
     float *scales = (float *)smem + W * 16 * LDJ + wave * NI * 16;
+    if constexpr (AHEAD) {
+        // The workgroup that follows on this XCD finds its rows of V, where
+        // they are no longer than 2 KB, on the way: one touch a cache line,
+        // shared among the workgroups that will use them.  They arrive during
+        // the epilogue; left to the next tile's own loads, which all miss at
+        // once when a band begins, such a tile took 35 us for 27 (32768 x
+        // 4096 x 1024 in bf16: 268 -> 260 us).
+        if (a.ldv <= 2048 && tile + kCUs < a.ti * a.tj) {
+            int ni, nj;
+            mm_tile(tile + kCUs, a.ti, a.tj, ni, nj);
+            const int shares = min(8, a.tj), rows = (BI + shares - 1) / shares, lines = ((int)a.ldv + 127) / 128;
+            const i32x4 rs = make_rsrc(a.V + (long)ni * BI * a.ldv, (uint32_t)min(BI, a.I - ni * BI) * (uint32_t)a.ldv);
+            const uint32_t at = lds0 + W * 16 * LDJ * 4 + WJ * BI * 4 + wave * 256;
+            for (int n = 0; n < rows * lines; n += W * 64) {
+                const int u = n + wave * 64 + lane, row = (nj % shares) * rows + u / lines;
+                lds_touch(__builtin_amdgcn_readfirstlane(at),
+                          u < rows * lines ? (uint32_t)row * (uint32_t)a.ldv + (u % lines) * 128 : kOutOfRange, rs);
+            }
+        }
+    }
     constexpr int LPR = NJ * 2, RPP = 64 / LPR, Q = 16 / RPP;  // lanes per row, rows per pass, passes
     const int r = lane & 15, g = lane >> 4, c8 = (lane % LPR) * 8, rr = lane / LPR;
     const int j = j0 + wj + c8, ib = i0 + wi + rr;
@@ -555,6 +580,7 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
             }
         }
     }
+    if (AHEAD) mm_wait<0>();  // nothing may reach LDS after the workgroup's end
 }
 
 // Grid: x = tiles, y = splits of k.
@@ -776,8 +802,6 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
 
 // ---- host side ----------------------------------------------------------------
 
-constexpr int kCUs = 256;
-
 // How a product of I x J over `slabs` slabs is cut: a tile size and a number
 // of splits of k, the pair with the least estimated time.  The estimate is a
 // fit to measured launches (bf16 and e4m3, all operand orders, 1 to 2600
@@ -899,6 +923,11 @@ static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t 
     return e != hipSuccess ? e : mm_join(a, p, ep, part, st);
 }
 
+// Whether an output of I x J is larger than the eight L2 caches of 4 MB.
+// Non-temporal stores then leave them to the operands: 32768 x 4096 x 1024 in
+// bf16 260 -> 249 us, 32768 x 1024 x 4096 in e4m3 121 -> 118.
+static bool past_caches(int I, int J, bool f32) { return (size_t)I * J * (f32 ? 4 : 2) > ((size_t)32 << 20); }
+
 size_t linear_ws_bytes(int M, int N, int K, bool f8) {
     if (mv_takes(M, N)) return 0;
     return mm_part_bytes(mm_plan(M, N, slabs_of(K, f8)), M, N);
@@ -912,7 +941,7 @@ hipError_t launch_linear(const void *x, const void *w, const float *xs, const fl
     a.V = (const char *)x; a.U = (const char *)w;
     a.ldv = a.ldu = K * es;
     a.I = M; a.J = N; a.K = K; a.parts = 1;
-    const Epilogue ep{xs, ws, bias, residual, y, (uint16_t *)z, N, act, y_f32};
+    const Epilogue ep{xs, ws, bias, residual, y, (uint16_t *)z, N, act, y_f32, past_caches(M, N, y_f32)};
     if (mv_takes(M, N))
         return f8 ? mv_run<true>(x, w, M, N, K, ep, st) : mv_run<false>(x, w, M, N, K, ep, st);
     if (!f8) return mm_run<false, false, MM_BF16>(a, ep, part, st);
@@ -996,8 +1025,8 @@ hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const
     a.ldu = b.ldu = (long)K * 2;
     a.I = M; a.J = K; a.K = N;
     b.I = N; b.J = K; b.K = M;
-    const Epilogue ea{nullptr, nullptr, nullptr, nullptr, dx, nullptr, K, ACT_NONE, grad_f32};
-    const Epilogue eb{nullptr, nullptr, nullptr, nullptr, dw, nullptr, K, ACT_NONE, grad_f32};
+    const Epilogue ea{nullptr, nullptr, nullptr, nullptr, dx, nullptr, K, ACT_NONE, grad_f32, past_caches(M, K, grad_f32)};
+    const Epilogue eb{nullptr, nullptr, nullptr, nullptr, dw, nullptr, K, ACT_NONE, grad_f32, past_caches(N, K, grad_f32)};
     if (p.pair) {
         const MmPlan qa = mm_set(a, false), qb = mm_set(b, false);
         const int na = a.ti * a.tj * qa.splits, nb = b.ti * b.tj * qb.splits;

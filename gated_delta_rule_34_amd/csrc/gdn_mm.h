@@ -83,6 +83,14 @@ __device__ __forceinline__ void lds_load(uint32_t lds, uint32_t voff, i32x4 rsrc
                  : "m0", "memory");
 }
 
+// The same with 4 bytes a lane: for what it brings into the caches.
+__device__ __forceinline__ void lds_touch(uint32_t lds, uint32_t voff, i32x4 rsrc) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "m0", "memory");
+}
+
 __device__ __forceinline__ i32x4 make_rsrc(const char *base, uint32_t bytes) {
     const uint64_t b = (uint64_t)base;
     i32x4 r;

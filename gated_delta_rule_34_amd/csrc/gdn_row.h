@@ -103,6 +103,15 @@ __device__ __forceinline__ void store8nt(uint16_t *p, const f32x8 &v) {
     for (int e = 0; e < 4; ++e) u[e] = pack2_bf16(v[2 * e], v[2 * e + 1]);
     __builtin_nontemporal_store(u, (u32x4_a2 *)p);
 }
+__device__ __forceinline__ void store8nt(float *p, const f32x8 &v) {
+    __builtin_nontemporal_store(f32x4_a4{v[0], v[1], v[2], v[3]}, (f32x4_a4 *)p);
+    __builtin_nontemporal_store(f32x4_a4{v[4], v[5], v[6], v[7]}, (f32x4_a4 *)(p + 4));
+}
+template <class T>
+__device__ __forceinline__ void store8p(T *p, const f32x8 &v, bool nt) {
+    if (nt) store8nt(p, v);
+    else store8v(p, v);
+}
 template <class T>
 __device__ __forceinline__ f32x8 load8v(const T *p, int c, int D) {
     if (c + 8 <= D) return load8v(p + c);
