@@ -590,14 +590,41 @@ __global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, 
     mm_body<BI, BJ, WI, WJ, NBUF, TV, TU, MODE>(smem, a, ep, part, blockIdx.x, blockIdx.y);
 }
 
-// Both products of the backward in one launch, where neither fills the card:
-// workgroups 0 .. na - 1 are dx's tiles and splits, the others dw's.
+// dbias from n rows of partial column sums [n, J], 32 columns a workgroup.
+struct ColSums {
+    const float *sums;
+    float *out;
+    int n, J;
+};
+
+__device__ __forceinline__ void colsum_body(char *smem, const ColSums &c, int group) {
+    float(*sh)[33] = (float(*)[33])smem;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, j = group * 32 + tx;
+    float v = 0.f;
+    if (j < c.J) {
+#pragma unroll 8
+        for (int i = ty; i < c.n; i += 8) v += c.sums[(long)i * c.J + j];
+    }
+    sh[ty][tx] = v;
+    __syncthreads();
+    if (ty == 0 && j < c.J) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sh[i][tx];
+        c.out[j] = s;
+    }
+}
+
+// Both products of the backward in one launch, where they fit the card
+// together: workgroups 0 .. na - 1 are dx's tiles and splits, the next nb dw's,
+// those after them add up dbias.
 template <int NBUF>
 __global__ __launch_bounds__(256) void mm_pair_kernel(MmArgs a, Epilogue ea, float *pa, int na, MmArgs b, Epilogue eb,
-                                                      float *pb) {
+                                                      float *pb, int nb, ColSums c) {
     __shared__ __attribute__((aligned(1024))) char smem[mm_lds<128, 128, 2, 2, NBUF>()];
     const int g = blockIdx.x, ta = a.ti * a.tj, tb = b.ti * b.tj;
-    if (g < na) mm_body<128, 128, 2, 2, NBUF, false, true, MM_BF16>(smem, a, ea, pa, g % ta, g / ta);
+    if (g >= na + nb) colsum_body(smem, c, g - na - nb);
+    else if (g < na) mm_body<128, 128, 2, 2, NBUF, false, true, MM_BF16>(smem, a, ea, pa, g % ta, g / ta);
     else mm_body<128, 128, 2, 2, NBUF, true, true, MM_BF16>(smem, b, eb, pb, (g - na) % tb, (g - na) / tb);
 }
 
@@ -1008,7 +1035,7 @@ hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (out) dz = out;
-        if (dbias) {
+        if (dbias && !p.pair) {
             e = launch_colsum(sums, dbias, p.blocks, N, st);
             if (e != hipSuccess) return e;
         }
@@ -1031,10 +1058,12 @@ hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const
         const MmPlan qa = mm_set(a, false), qb = mm_set(b, false);
         const int na = a.ti * a.tj * qa.splits, nb = b.ti * b.tj * qb.splits;
         float *sa = qa.splits > 1 ? pa : nullptr, *sb = qb.splits > 1 ? pb : nullptr;
+        const ColSums c{(const float *)(ws + p.sums_off), dbias, p.blocks, N};
+        const dim3 grid((unsigned)(na + nb + (dbias ? (N + 31) / 32 : 0)));
         if (p.deep)
-            hipLaunchKernelGGL((mm_pair_kernel<4>), dim3((unsigned)(na + nb)), dim3(256), 0, st, a, ea, sa, na, b, eb, sb);
+            hipLaunchKernelGGL((mm_pair_kernel<4>), grid, dim3(256), 0, st, a, ea, sa, na, b, eb, sb, nb, c);
         else
-            hipLaunchKernelGGL((mm_pair_kernel<2>), dim3((unsigned)(na + nb)), dim3(256), 0, st, a, ea, sa, na, b, eb, sb);
+            hipLaunchKernelGGL((mm_pair_kernel<2>), grid, dim3(256), 0, st, a, ea, sa, na, b, eb, sb, nb, c);
         e = hipGetLastError();
         if (e == hipSuccess) e = mm_join(a, qa, ea, pa, st);
         return e != hipSuccess ? e : mm_join(b, qb, eb, pb, st);
