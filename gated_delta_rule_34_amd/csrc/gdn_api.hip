@@ -697,7 +697,7 @@ static gdn_status linear_check(int M, int N, int K, gdn_dtype dtype) {
 
 size_t gdn_linear_workspace(int M, int N, int K, gdn_dtype dtype) {
     if (linear_check(M, N, K, dtype) != GDN_OK) return 0;
-    return align_up(gdn::linear_ws_bytes(M, N, K, dtype == GDN_F8E4M3));
+    return align_up(gdn::linear_ws_bytes(gdn::linear_plan(M, N, K, dtype == GDN_F8E4M3), M, N));
 }
 
 gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const float *w_scale, const float *bias,
@@ -712,7 +712,8 @@ gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const 
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(residual, 16) || !aligned(y, 16) || !aligned(z, 16) ||
         !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))
         return GDN_ERR_INVALID_ARG;
-    const size_t need = gdn_linear_workspace(M, N, K, dtype);
+    const gdn::MmPlan plan = gdn::linear_plan(M, N, K, f8);
+    const size_t need = align_up(gdn::linear_ws_bytes(plan, M, N));
     if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
     const size_t mn = (size_t)M * N;
     const Range ins[] = {{x, (size_t)M * K * esize3(dtype)}, {w, (size_t)N * K * esize3(dtype)},
@@ -720,7 +721,7 @@ gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const 
                          {residual == y ? nullptr : residual, mn * esize3(out_dtype)}};
     const Range outs[] = {{y, mn * esize3(out_dtype)}, {z, mn * 2}, {need ? ws : nullptr, need}};
     if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
-    return from_hip(gdn::launch_linear(x, w, x_scale, w_scale, bias, residual, y, z, M, N, K, f8, out_dtype == GDN_F32,
+    return from_hip(gdn::launch_linear(plan, x, w, x_scale, w_scale, bias, residual, y, z, M, N, K, f8, out_dtype == GDN_F32,
                                        (int)act, (float *)ws, (hipStream_t)stream));
 }
 
@@ -744,15 +745,16 @@ gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const vo
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 16) || !aligned(dx, 16) ||
         !aligned(dw, 16) || !aligned(dbias, 4))
         return GDN_ERR_INVALID_ARG;
-    const size_t need = gdn_linear_bwd_workspace(M, N, K, dy_dtype, grad_dtype, act, dx != nullptr, dw != nullptr,
-                                                 dbias != nullptr);
+    const gdn::LinearBwdPlan plan = gdn::linear_bwd_plan(M, N, K, dy_dtype == GDN_F32, grad_dtype == GDN_F32, (int)act,
+                                                         dx != nullptr, dw != nullptr, dbias != nullptr);
+    const size_t need = plan.total;
     if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
     const size_t mn = (size_t)M * N, mk = (size_t)M * K, nk = (size_t)N * K;
     const Range ins[] = {{dy, mn * esize3(dy_dtype)}, {x, mk * 2}, {w, nk * 2}, {z, mn * 2}};
     const Range outs[] = {{dx, mk * esize3(grad_dtype)}, {dw, nk * esize3(grad_dtype)}, {dbias, (size_t)N * 4},
                           {need ? ws : nullptr, need}};
     if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
-    return from_hip(gdn::launch_linear_bwd(dy, x, w, z, dx, dw, dbias, M, N, K, dy_dtype == GDN_F32,
+    return from_hip(gdn::launch_linear_bwd(plan, dy, x, w, z, dx, dw, dbias, M, N, K, dy_dtype == GDN_F32,
                                            grad_dtype == GDN_F32, (int)act, (char *)ws, (hipStream_t)stream));
 }
 

@@ -148,15 +148,22 @@ hipError_t launch_add_rmsnorm_bwd(const void *dy, const void *r, const float *w,
 // out[c] = sum of n rows of part [n, D], in a fixed order.
 hipError_t launch_colsum(const float *part, float *out, int n, int D, hipStream_t st);
 
+// How a product is cut: tile edge (0: the kernel for few rows or columns),
+// splits of k and slabs in each, four buffers or two.
+struct MmPlan {
+    int tile, splits, per_split;
+    bool deep;
+};
 // The layer's matrix products (gdn_linear.hip): y = act((x w^T) xs ws + bias)
 // + residual, z = the activation's argument; x [M, K], w [N, K] in bf16 or
 // (f8) e4m3, y and residual bf16 or (y_f32) fp32, z bf16.  part:
 // linear_ws_bytes() bytes of partial sums (0: none needed).  act: 0 none,
 // 1 relu, 2 silu, 3 gelu.
-size_t linear_ws_bytes(int M, int N, int K, bool f8);
-hipError_t launch_linear(const void *x, const void *w, const float *xs, const float *ws, const float *bias,
-                         const void *residual, void *y, void *z, int M, int N, int K, bool f8, bool y_f32, int act,
-                         float *part, hipStream_t st);
+MmPlan linear_plan(int M, int N, int K, bool f8);
+size_t linear_ws_bytes(const MmPlan &p, int M, int N);
+hipError_t launch_linear(const MmPlan &p, const void *x, const void *w, const float *xs, const float *ws,
+                         const float *bias, const void *residual, void *y, void *z, int M, int N, int K, bool f8,
+                         bool y_f32, int act, float *part, hipStream_t st);
 // Its backward (bf16 x and w): dz = dy act'(z) in bf16 planes (one, or three
 // for fp32 gradients of an inexact dz) where it is not dy itself; dx, dw
 // (nullable) in bf16 or (grad_f32) fp32; dbias (nullable) fp32.
@@ -164,11 +171,12 @@ struct LinearBwdPlan {
     int Np, planes, blocks;   // columns of a plane; planes; partial rows of dbias
     bool copy;                // dz is written to the workspace
     bool pair, deep;          // both products in one launch; four buffers each
+    MmPlan dx, dw;
     size_t plane, sums_off, part_off, part2_off, total;
 };
 LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, int act, bool dx, bool dw, bool dbias);
-hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,
-                             float *dbias, int M, int N, int K, bool dy_f32, bool grad_f32, int act, char *ws,
-                             hipStream_t st);
+hipError_t launch_linear_bwd(const LinearBwdPlan &p, const void *dy, const void *x, const void *w, const void *z,
+                             void *dx, void *dw, float *dbias, int M, int N, int K, bool dy_f32, bool grad_f32, int act,
+                             char *ws, hipStream_t st);
 
 }  // namespace gdn

@@ -839,11 +839,6 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
 // work; splits cost a second launch of 3 us and 8 bytes of partial sum per
 // output and split at 7 TB/s (they come back from the caches).  Four buffers
 // against two at 1024 x 4096 x 4096: 38.9 and 47.3 us.
-struct MmPlan {
-    int tile, splits, per_split;
-    bool deep;  // one workgroup per compute unit, four buffers (128-tile)
-};
-
 static double mm_round_us(int tile, long n, int per) {  // n workgroups, at most one round
     if (tile == 256) return per * (1.2 + 0.35 * n / kCUs);
     return n <= kCUs ? 2.5 + per * (0.42 + 0.1 * n / kCUs) : per * (0.62 + 0.32 * (n - kCUs) / kCUs);
@@ -855,12 +850,18 @@ static MmPlan mm_plan(int I, int J, int slabs) {
     for (const int tile : {256, 128}) {
         const long tiles = (long)((I + tile - 1) / tile) * ((J + tile - 1) / tile);
         const long at_once = tile == 256 ? kCUs : 2 * kCUs;
-        for (int s = 1; s <= 32 && s * 2 <= (slabs > 2 ? slabs : 2); ++s) {
+        // more splits than fill the card once only add partial sums
+        for (int s = 1; s <= 32 && (s == 1 || (s * 2 <= slabs && tiles * s <= at_once)); ++s) {
             const int per = (slabs + s - 1) / s;
-            if ((slabs + per - 1) / per != s) continue;  // the same cut as a smaller s
+            if (s > 1 && (slabs + per - 1) / per != s) continue;  // the same cut as a smaller s
             const long n = tiles * s;
-            double us = 4.0 + (double)(n / at_once) * (mm_round_us(tile, at_once, per) + 2.0);
-            if (n % at_once) us += mm_round_us(tile, n % at_once, per);
+            double us = 4.0;
+            if (n <= at_once) {
+                us += mm_round_us(tile, n, per);
+            } else {
+                us += (double)(n / at_once) * (mm_round_us(tile, at_once, per) + 2.0);
+                if (n % at_once) us += mm_round_us(tile, n % at_once, per);
+            }
             if (s > 1) us += 3.0 + 8.0 * s * I * J / 7e6;
             if (us < least) {
                 least = us;
@@ -917,13 +918,11 @@ static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, cons
 static int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
 
 // Fills in what the plan decides.
-static MmPlan mm_set(MmArgs &a, bool f8) {
+static void mm_set(MmArgs &a, const MmPlan &p, bool f8) {
     a.slabs = a.parts * slabs_of(a.K, f8);
-    const MmPlan p = mm_plan(a.I, a.J, a.slabs);
     a.per_split = p.per_split;
     a.ti = (a.I + p.tile - 1) / p.tile;
     a.tj = (a.J + p.tile - 1) / p.tile;
-    return p;
 }
 
 static hipError_t mm_join(const MmArgs &a, const MmPlan &p, const Epilogue &ep, const float *part, hipStream_t st) {
@@ -936,8 +935,8 @@ static hipError_t mm_join(const MmArgs &a, const MmPlan &p, const Epilogue &ep, 
 }
 
 template <bool TV, bool TU, int MODE>
-static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t st) {
-    const MmPlan p = mm_set(a, MODE != MM_BF16);
+static hipError_t mm_run(MmArgs a, const MmPlan &p, const Epilogue &ep, float *part, hipStream_t st) {
+    mm_set(a, p, MODE != MM_BF16);
     const dim3 grid((unsigned)(a.ti * a.tj), (unsigned)p.splits);
     float *pp = p.splits > 1 ? part : nullptr;
     if (p.tile == 256)
@@ -955,24 +954,26 @@ static hipError_t mm_run(MmArgs a, const Epilogue &ep, float *part, hipStream_t 
 // bf16 260 -> 249 us, 32768 x 1024 x 4096 in e4m3 121 -> 118.
 static bool past_caches(int I, int J, bool f32) { return (size_t)I * J * (f32 ? 4 : 2) > ((size_t)32 << 20); }
 
-size_t linear_ws_bytes(int M, int N, int K, bool f8) {
-    if (mv_takes(M, N)) return 0;
-    return mm_part_bytes(mm_plan(M, N, slabs_of(K, f8)), M, N);
+MmPlan linear_plan(int M, int N, int K, bool f8) {
+    return mv_takes(M, N) ? MmPlan{0, 1, 0, false} : mm_plan(M, N, slabs_of(K, f8));
 }
 
-hipError_t launch_linear(const void *x, const void *w, const float *xs, const float *ws, const float *bias,
-                         const void *residual, void *y, void *z, int M, int N, int K, bool f8, bool y_f32, int act,
-                         float *part, hipStream_t st) {
+size_t linear_ws_bytes(const MmPlan &p, int M, int N) { return mm_part_bytes(p, M, N); }
+
+hipError_t launch_linear(const MmPlan &p, const void *x, const void *w, const float *xs, const float *ws,
+                         const float *bias, const void *residual, void *y, void *z, int M, int N, int K, bool f8,
+                         bool y_f32, int act, float *part, hipStream_t st) {
     MmArgs a{};
     const long es = f8 ? 1 : 2;
     a.V = (const char *)x; a.U = (const char *)w;
     a.ldv = a.ldu = K * es;
     a.I = M; a.J = N; a.K = K; a.parts = 1;
     const Epilogue ep{xs, ws, bias, residual, y, (uint16_t *)z, N, act, y_f32, past_caches(M, N, y_f32)};
-    if (mv_takes(M, N))
+    if (p.tile == 0)
         return f8 ? mv_run<true>(x, w, M, N, K, ep, st) : mv_run<false>(x, w, M, N, K, ep, st);
-    if (!f8) return mm_run<false, false, MM_BF16>(a, ep, part, st);
-    return y_f32 ? mm_run<false, false, MM_F8_F32>(a, ep, part, st) : mm_run<false, false, MM_F8>(a, ep, part, st);
+    if (!f8) return mm_run<false, false, MM_BF16>(a, p, ep, part, st);
+    return y_f32 ? mm_run<false, false, MM_F8_F32>(a, p, ep, part, st)
+                 : mm_run<false, false, MM_F8>(a, p, ep, part, st);
 }
 
 // Rows of dz per workgroup of dz_kernel: about 2048 workgroups, whole groups of
@@ -998,7 +999,7 @@ LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, i
     p.blocks = (M + rows - 1) / rows;
     if (dbias) off += up((size_t)p.blocks * N * 4);
     p.part_off = off;
-    MmPlan a{}, b{};
+    MmPlan &a = p.dx, &b = p.dw;
     if (dx) a = mm_plan(M, K, p.planes * slabs_of(N, false));
     if (dw) b = mm_plan(N, K, p.planes * slabs_of(M, false));
     const size_t pa = dx ? up(mm_part_bytes(a, M, K)) : 0, pb = dw ? up(mm_part_bytes(b, N, K)) : 0;
@@ -1013,10 +1014,9 @@ LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, i
     return p;
 }
 
-hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,
-                             float *dbias, int M, int N, int K, bool dy_f32, bool grad_f32, int act, char *ws,
-                             hipStream_t st) {
-    const LinearBwdPlan p = linear_bwd_plan(M, N, K, dy_f32, grad_f32, act, dx, dw, dbias);
+hipError_t launch_linear_bwd(const LinearBwdPlan &p, const void *dy, const void *x, const void *w, const void *z,
+                             void *dx, void *dw, float *dbias, int M, int N, int K, bool dy_f32, bool grad_f32, int act,
+                             char *ws, hipStream_t st) {
     const uint16_t *dz = (const uint16_t *)dy;
     hipError_t e = hipSuccess;
     if (p.copy || dbias) {
@@ -1055,7 +1055,9 @@ hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const
     const Epilogue ea{nullptr, nullptr, nullptr, nullptr, dx, nullptr, K, ACT_NONE, grad_f32, past_caches(M, K, grad_f32)};
     const Epilogue eb{nullptr, nullptr, nullptr, nullptr, dw, nullptr, K, ACT_NONE, grad_f32, past_caches(N, K, grad_f32)};
     if (p.pair) {
-        const MmPlan qa = mm_set(a, false), qb = mm_set(b, false);
+        const MmPlan &qa = p.dx, &qb = p.dw;
+        mm_set(a, qa, false);
+        mm_set(b, qb, false);
         const int na = a.ti * a.tj * qa.splits, nb = b.ti * b.tj * qb.splits;
         float *sa = qa.splits > 1 ? pa : nullptr, *sb = qb.splits > 1 ? pb : nullptr;
         const ColSums c{(const float *)(ws + p.sums_off), dbias, p.blocks, N};
@@ -1068,8 +1070,8 @@ hipError_t launch_linear_bwd(const void *dy, const void *x, const void *w, const
         if (e == hipSuccess) e = mm_join(a, qa, ea, pa, st);
         return e != hipSuccess ? e : mm_join(b, qb, eb, pb, st);
     }
-    if (dx) e = mm_run<false, true, MM_BF16>(a, ea, pa, st);
-    if (dw && e == hipSuccess) e = mm_run<true, true, MM_BF16>(b, eb, pb, st);
+    if (dx) e = mm_run<false, true, MM_BF16>(a, p.dx, ea, pa, st);
+    if (dw && e == hipSuccess) e = mm_run<true, true, MM_BF16>(b, p.dw, eb, pb, st);
     return e;
 }
 
