@@ -631,6 +631,13 @@ def _scratch(nbytes, device):
     return ws if ws.data_ptr() % 256 == 0 else _workspace(nbytes, device)[1]
 
 
+def _given(ws, dev):
+    """Size in bytes of a workspace that the caller hands in."""
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}, got {ws.device}")
+    return ws.numel() * ws.element_size()
+
+
 _current = None
 
 
@@ -695,7 +702,7 @@ def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-5, out_dtype=None, return_r
     y_scale = torch.empty(shape[:-1], dtype=f32, device=dev) if odt == torch.float8_e4m3fn else None
     _on_device(load().gdn_add_rmsnorm, "gdn_add_rmsnorm", dev,
                _addr(x), _addr(residual), _addr(weight), _addr(y), _addr(r), _addr(rstd), _addr(y_scale), rows, D,
-                _code(x.dtype, "x"), _code(rdt, "residual"), _code(odt, "out_dtype"), float(eps))
+               _code(x.dtype, "x"), _code(rdt, "residual"), _code(odt, "out_dtype"), float(eps))
     return y, r, rstd, y_scale
 
 
@@ -725,12 +732,14 @@ def gdn_add_rmsnorm_bwd(dy, r, weight, rstd, dr=None, need_dweight=True, workspa
     lib = load()
     if need_dweight:
         dw = torch.empty((D,), dtype=f32, device=dev)
-        need = lib.gdn_add_rmsnorm_bwd_workspace(rows, D)
-        ws = workspace if workspace is not None else _scratch(need, dev)
-        nbytes = ws.numel() * ws.element_size()
+        if workspace is None:
+            nbytes = lib.gdn_add_rmsnorm_bwd_workspace(rows, D)
+            ws = _scratch(nbytes, dev)
+        else:
+            ws, nbytes = workspace, _given(workspace, dev)
     _on_device(lib.gdn_add_rmsnorm_bwd, "gdn_add_rmsnorm_bwd", dev,
                _addr(dy), _addr(r), _addr(weight), _addr(rstd), _addr(dr), _addr(dx), _addr(dw), rows, D,
-                _code(dy.dtype, "dy"), _code(r.dtype, "r"), _addr(ws), nbytes)
+               _code(dy.dtype, "dy"), _code(r.dtype, "r"), _addr(ws), nbytes)
     return dx, dw
 
 
@@ -804,16 +813,16 @@ def gdn_linear(x, weight, bias=None, residual=None, act="none", x_scale=None, w_
     z = torch.empty(shape, dtype=torch.bfloat16, device=dev) if return_preact else None
     lib = load()
     code, ocode = _code(dt, "x"), _code(odt, "out_dtype")
-    ws, nbytes = workspace, 0
+    ws = workspace
     if ws is None:
-        need = lib.gdn_linear_workspace(M, N, K, code)
-        if need:
-            ws = _scratch(need, dev)
-    if ws is not None:
-        nbytes = ws.numel() * ws.element_size()
+        nbytes = lib.gdn_linear_workspace(M, N, K, code)
+        if nbytes:
+            ws = _scratch(nbytes, dev)
+    else:
+        nbytes = _given(ws, dev)
     _on_device(lib.gdn_linear, "gdn_linear", dev,
                _addr(x), _addr(weight), _addr(x_scale), _addr(w_scale), _addr(bias), _addr(residual), _addr(y),
-                _addr(z), M, N, K, code, ocode, _act_code(act), _addr(ws), nbytes)
+               _addr(z), M, N, K, code, ocode, _act_code(act), _addr(ws), nbytes)
     return y, z
 
 
@@ -850,16 +859,16 @@ def gdn_linear_bwd(dy, x, weight, z=None, act="none", bias=False, grad_dtype=Non
     db = torch.empty((N,), dtype=torch.float32, device=dev) if bias else None
     lib = load()
     a, dyc, gc = _act_code(act), _code(dy.dtype, "dy"), _code(gdt, "grad_dtype")
-    ws, nbytes = workspace, 0
+    ws = workspace
     if ws is None:
-        need = lib.gdn_linear_bwd_workspace(M, N, K, dyc, gc, a, int(need_dx), int(need_dw), int(bool(bias)))
-        if need:
-            ws = _scratch(need, dev)
-    if ws is not None:
-        nbytes = ws.numel() * ws.element_size()
+        nbytes = lib.gdn_linear_bwd_workspace(M, N, K, dyc, gc, a, int(need_dx), int(need_dw), int(bool(bias)))
+        if nbytes:
+            ws = _scratch(nbytes, dev)
+    else:
+        nbytes = _given(ws, dev)
     _on_device(lib.gdn_linear_bwd, "gdn_linear_bwd", dev,
                _addr(dy), _addr(x), _addr(weight), _addr(z) if a else None, _addr(dx), _addr(dw), _addr(db), M, N, K,
-                dyc, gc, a, _addr(ws), nbytes)
+               dyc, gc, a, _addr(ws), nbytes)
     return dx, dw, db
 
 

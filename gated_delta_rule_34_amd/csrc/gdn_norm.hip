@@ -99,7 +99,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const XT *x
 // fixed order (no atomics, so results repeat bit for bit).  A row takes as long
 // as its loads, its sum and its stores one after the other, so the next row's
 // loads are issued before this row's sum (AHEAD; not at 1024 threads, whose
-// registers do not hold two rows): 32768 x 1024 in bf16 43.1 -> 39.6 us, 5.1 TB/s.
+// registers do not hold two rows): 32768 x 1024 in bf16 43.1 -> 39.6 us, 5.1
+// TB/s.  Beyond 8192 columns a few registers spill; the loads still bound it.
 template <class DT, class RT, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(const DT *dy, const RT *r, const float *w,
                                                                          const float *rstd, const RT *dr, RT *dx,

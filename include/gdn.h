@@ -377,6 +377,7 @@ gdn_status gdn_gated_rmsnorm(const float *o, const void *z, const float *weight,
  *   y = e4m3(u s weight / y_scale), rounded to nearest even
  * All of it in fp32 with one rounding per output; s is taken of the fp32 sum,
  * before r is rounded to its type.
+ * (The division by 448 is a product with 1 / 448 in fp32.)
  *   x        [rows, D] dtype (GDN_BF16 or GDN_F32)
  *   residual [rows, D] rdtype, nullable.  rdtype: GDN_F32, or GDN_BF16 with bf16 x
  *   weight   [D] fp32
@@ -423,13 +424,15 @@ gdn_status gdn_add_rmsnorm_bwd(const void *dy, const void *r, const float *weigh
  *   scale = max|x| / 448 (1 for a row of zeros);  q = e4m3(x / scale)
  *   x [rows, D] dtype (GDN_BF16 or GDN_F32), 16-byte aligned;
  *   q [rows, D] e4m3, 8-byte aligned;  scale [rows] fp32
+ * A row that holds a NaN has NaN as its scale and codes; one with an infinity
+ * has scale infinity, codes zero where the row is finite and NaN where not.
  * 1 <= D <= 32768.  Errors as gdn_add_rmsnorm.  Asynchronous; no workspace.
  */
 gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long rows, int D, gdn_dtype dtype,
                              void *stream);
 
 /* Activation of gdn_linear: none, max(z, 0), z sigmoid(z), z Phi(z) with the
- * normal distribution function Phi. */
+ * normal distribution function Phi (to 1e-7). */
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_RELU = 1, GDN_ACT_SILU = 2, GDN_ACT_GELU = 3 } gdn_act;
 
 /*

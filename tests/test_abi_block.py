@@ -191,3 +191,17 @@ def test_binding_refuses_wrong_tensors():
         gdn.gdn_quantize_rows(x.to(torch.float16))
     with pytest.raises(ValueError, match="at least one axis"):
         gdn.gdn_quantize_rows(torch.zeros(()))
+
+
+def test_binding_refuses_a_workspace_elsewhere():
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    x, w, ws = torch.zeros(4, 8, dtype=bf), torch.ones(8, 8, dtype=bf), torch.empty(1 << 16, device="meta")
+    with pytest.raises(ValueError, match="workspace must be"):
+        gdn.gdn_linear(x, w, workspace=ws)
+    with pytest.raises(ValueError, match="workspace must be"):
+        gdn.gdn_linear_bwd(x, x, w, workspace=ws)
+    with pytest.raises(ValueError, match="workspace must be"):
+        gdn.gdn_add_rmsnorm_bwd(x, x, torch.ones(8), torch.ones(4), workspace=ws)
+    with pytest.raises(ValueError, match="workspace must be"):
+        gdn.gdn_linear(x, w, workspace=torch.empty(64, 64)[:, :32])

@@ -270,6 +270,26 @@ def test_another_stream():
     assert torch.equal(dx, gdn.gdn_linear_bwd(want, x, w, need_dw=False)[0])
 
 
+def test_two_streams_at_once():
+    """Split sums and paired gradients on two streams, each call with its own workspace."""
+    rng = np.random.default_rng(27)
+    work = []
+    for _ in range(2):
+        x, w, dy = _ints(rng, (200, 4096), 2, BF), _ints(rng, (520, 4096), 2, BF), _ints(rng, (200, 520), 2, BF)
+        work.append((x, w, dy, gdn.gdn_linear(x, w, out_dtype=F32)[0], gdn.gdn_linear_bwd(dy, x, w, bias=True)))
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for k, (x, w, dy, _, _) in enumerate(work):
+            with torch.cuda.stream(side[k]):
+                got[k].append((gdn.gdn_linear(x, w, out_dtype=F32)[0], gdn.gdn_linear_bwd(dy, x, w, bias=True)))
+    torch.cuda.synchronize()
+    for k, (_, _, _, y, grads) in enumerate(work):
+        for a, b in got[k]:
+            assert torch.equal(a, y) and all(torch.equal(u, v) for u, v in zip(b, grads))
+
+
 @pytest.mark.parametrize("M,N", [(1_100_003, 2056), (2056, 1_100_003)])
 def test_offsets_past_2_to_the_31(M, N):
     """Outputs of 2.26e9 values: the corners against the same rows and columns computed alone."""
