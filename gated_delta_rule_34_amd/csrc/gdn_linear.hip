@@ -218,14 +218,15 @@ struct Epilogue {
 // to bf16, which holds them exactly, as they leave LDS.
 enum { MM_BF16 = 0, MM_F8 = 1, MM_F8_F32 = 2 };
 
-// One tile of one split of k, with NBUF slabs in LDS.  part (nullable): fp32 partial sums
-// [split, I, J] instead of the epilogue.
+// LDS of a workgroup: NBUF slabs; bias and w_scale of the tile's columns and
+// x_scale of its rows; 256 bytes a wave that touches write to.
 template <int BI, int BJ, int WI, int WJ, int NBUF>
-constexpr int mm_lds() {  // slabs, or the epilogue's image after them
-    constexpr int slabs = NBUF * (BI + BJ) * 128, image = WI * WJ * 16 * (BJ / WJ + 4) * 4 + WJ * BI * 4;
-    return slabs > image ? slabs : image;
+constexpr int mm_lds() {
+    return NBUF * (BI + BJ) * 128 + (2 * BJ + BI) * 4 + WI * WJ * 256;
 }
 
+// One tile of one split of k.  part (nullable): fp32 partial sums [split, I, J]
+// instead of the epilogue.
 template <int BI, int BJ, int WI, int WJ, int NBUF, bool TV, bool TU, int MODE>
 __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilogue &ep, float *part, int tile,
                                         int split) {
@@ -235,9 +236,7 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
     using SU = Stage<BJ, W, TU>;
     constexpr int SLAB = F8 ? 128 : 64;            // values of k per slab
     constexpr int BUF = SV::kBytes + SU::kBytes;
-    constexpr int LDJ = BJ / WJ + 4;               // floats per row of the epilogue's image
     constexpr bool AHEAD = BI == 256 && !TV;       // see the epilogue
-    static_assert(!AHEAD || W * 16 * LDJ * 4 + WJ * BI * 4 + W * 256 <= mm_lds<BI, BJ, WI, WJ, NBUF>(), "room");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int bi, bj;
     mm_tile(tile, a.ti, a.tj, bi, bj);
@@ -253,6 +252,24 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
     su.init(a.U, a.ldu, j0, a.J - j0, a.K, 0, per, p0, s0 - p0 * per, lane, wave);
     lds_cchar *lds = (lds_cchar *)smem;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+    // What the epilogue needs of the columns and rows, by way of LDS: loaded
+    // there, it would wait for the stores before it.  Issued before the slabs,
+    // it has landed when the first of them has.
+    const uint32_t aux0 = lds0 + NBUF * BUF, touch0 = aux0 + (2 * BJ + BI) * 4 + wave * 256;
+    const float *aux = (const float *)(smem + NBUF * BUF);
+    auto fetch = [&](const float *p, int at, int n, int valid) {
+        const i32x4 rs = make_rsrc((const char *)p, (uint32_t)min(n, valid) * 4);
+        for (int k = wave; k < n / 64; k += W)
+            lds_touch(__builtin_amdgcn_readfirstlane(aux0 + at * 4 + k * 256), (k * 64 + lane) * 4, rs);
+    };
+    if (!part) {
+        if (ep.bias) fetch(ep.bias + j0, 0, BJ, a.J - j0);
+        if (F8) {
+            fetch(ep.ws + j0, BJ, BJ, a.J - j0);
+            fetch(ep.xs + i0, 2 * BJ, BI, a.I - i0);
+        }
+    }
 
     f32x4 acc[NJ][NI];
 #pragma unroll
@@ -475,13 +492,15 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
         mm_wait<0>();
     }
 
-    // Epilogue: 16 rows of the wave's part of the tile at a time through LDS
-    // (its own region), so that a lane holds eight consecutive columns and a
-    // row's stores are contiguous.  Where the tile's columns are whole, what
-    // the rows add is fetched ahead of the products' way through LDS.
-    __syncthreads();
-    float *img = (float *)smem + wave * 16 * LDJ;
-    float *scales = (float *)smem + W * 16 * LDJ + wave * NI * 16;
+    // Epilogue, from the accumulators to memory: a lane holds four columns of
+    // a row in each 16-wide tile.  Exchanged between lanes 16 apart, two tiles
+    // give it eight consecutive ones; exchanged between the lanes of an even
+    // row and the next one, four tiles give a row's 64 columns, in bf16 a
+    // cache line, to eight lanes.
+#pragma unroll
+    for (int x = 0; x < NJ; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y) asm volatile("" : "+v"(acc[x][y]));
     if constexpr (AHEAD) {
         // The workgroup that follows on this XCD finds its rows of V, where
         // they are no longer than 2 KB, on the way: one touch a cache line,
@@ -494,93 +513,93 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
             mm_tile(tile + kCUs, a.ti, a.tj, ni, nj);
             const int shares = min(8, a.tj), rows = (BI + shares - 1) / shares, lines = ((int)a.ldv + 127) / 128;
             const i32x4 rs = make_rsrc(a.V + (long)ni * BI * a.ldv, (uint32_t)min(BI, a.I - ni * BI) * (uint32_t)a.ldv);
-            const uint32_t at = lds0 + W * 16 * LDJ * 4 + WJ * BI * 4 + wave * 256;
             for (int n = 0; n < rows * lines; n += W * 64) {
                 const int u = n + wave * 64 + lane, row = (nj % shares) * rows + u / lines;
-                lds_touch(__builtin_amdgcn_readfirstlane(at),
+                lds_touch(__builtin_amdgcn_readfirstlane(touch0),
                           u < rows * lines ? (uint32_t)row * (uint32_t)a.ldv + (u % lines) * 128 : kOutOfRange, rs);
             }
         }
     }
-    constexpr int LPR = NJ * 2, RPP = 64 / LPR, Q = 16 / RPP;  // lanes per row, rows per pass, passes
-    const int r = lane & 15, g = lane >> 4, c8 = (lane % LPR) * 8, rr = lane / LPR;
-    const int j = j0 + wj + c8, ib = i0 + wi + rr;
-    // (the loops below stay loops: unrolled, their code is longer than the
-    // instruction cache)
-    auto put = [&](int y) {
-        mm_fence();
+    constexpr int NQ = NJ / 4, TURNS = NQ * NI;  // a turn: 64 columns of a row tile
+    const int r = lane & 15, g = lane >> 4;
+    const int jl = wj + 32 * (r & 1) + 16 * (g & 1) + 8 * (g >> 1), il = wi + (r & ~1);
+    // (the loops over turns stay loops: unrolled, their code is longer than
+    // the instruction cache)
+    // v: the lane's columns of rows il and il + 1
+    auto pick = [&](f32x8 (&v)[2], int t) {
+        f32x4 p[4];
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            if (k == y) {
+        for (int k = 0; k < TURNS; ++k) {
+            if (k == t) {
 #pragma unroll
-                for (int x = 0; x < NJ; ++x) *(f32x4 *)(img + r * LDJ + 16 * x + 4 * g) = acc[x][k];
+                for (int q = 0; q < 4; ++q) p[q] = acc[4 * (k % NQ) + q][k / NQ];
                 // distinct per case: merged, the accumulators would be
                 // indexed at run time, that is, moved to scratch memory
-                asm volatile("; rows %0" ::"n"(k));
+                asm volatile("; turn %0" ::"n"(k));
             }
         }
-        mm_fence();  // other lanes' values are read next; a wave's LDS accesses are done in order
+        const bool odd = r & 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // the odd rows of 16 lanes of the first and the even ones of the second change places
+            const auto a0 = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[0][e]), __float_as_uint(p[1][e]), false, false);
+            const auto a1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[2][e]), __float_as_uint(p[3][e]), false, false);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t got = dpp_u32<0xb1, 0xf>(odd ? a0[h] : a1[h]);  // from the neighbouring lane
+                v[0][4 * h + e] = __uint_as_float(odd ? got : a0[h]);
+                v[1][4 * h + e] = __uint_as_float(odd ? a1[h] : got);
+            }
+        }
     };
-    auto get = [&](int q) {
-        const float *src = img + (q * RPP + rr) * LDJ + c8;
-        const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 4);
-        return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    };
-    auto rows = [&](auto res, const Epilogue::Cols &c) {
+    auto col = [&](int t) { return j0 + jl + 64 * (t % NQ); };
+    auto row = [&](int t) { return i0 + il + 16 * (t / NQ); };
+    auto turns = [&](auto res) {
         constexpr bool RES = decltype(res)::value;
+        Epilogue::Row o[2];
+        auto fetch_rows = [&](int t) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) o[q] = ep.row(min(row(t) + q, a.I - 1), col(t));
+        };
+        if (RES) fetch_rows(0);
 #pragma unroll 1
-        for (int y = 0; y < NI; ++y) {
-            Epilogue::Row o[Q];
-            if (RES) {
+        for (int t = 0; t < TURNS; ++t) {
+            f32x8 v[2];
+            pick(v, t);
+            const Epilogue::Row now[2] = {o[0], o[1]};
+            if (RES && t + 1 < TURNS) fetch_rows(t + 1);  // ahead of this turn's stores
+            const float *ca = aux + jl + 64 * (t % NQ);
+            Epilogue::Cols c;
+            if (ep.bias) c.b = load8v(ca);
+            if (F8) {
+                c.s = load8v(ca + BJ);
 #pragma unroll
-                for (int q = 0; q < Q; ++q) o[q] = ep.row(min(ib + 16 * y + q * RPP, a.I - 1), j);
+                for (int q = 0; q < 2; ++q) v[q] *= aux[2 * BJ + il + 16 * (t / NQ) + q];
             }
-            put(y);
-#pragma unroll
-            for (int q = 0; q < Q; q += 2) {  // two at a time: four do not fit the registers
-                f32x8 v[2] = {get(q), get(q + 1)};
-                if (F8) {
-                    v[0] *= scales[16 * y + q * RPP + rr];
-                    v[1] *= scales[16 * y + (q + 1) * RPP + rr];
-                }
-                const Epilogue::Row o2[2] = {o[q], o[q + 1]};
-                ep.whole<F8, RES>(v, c, o2, ib + 16 * y + q * RPP, RPP, j, a.I);
-            }
+            ep.whole<F8, RES>(v, c, now, row(t), 1, col(t), a.I);
         }
     };
     if (part) {
         part += (long)split * a.I * a.J;
 #pragma unroll 1
-        for (int y = 0; y < NI; ++y) {
-            put(y);
-#pragma unroll 1
-            for (int q = 0; q < Q; ++q) {
-                const int i = ib + 16 * y + q * RPP;
-                const f32x8 v = get(q);
-                if (i < a.I && j < a.J) store8v(part + (long)i * a.J, v, j, a.J);
-            }
+        for (int t = 0; t < TURNS; ++t) {
+            f32x8 v[2];
+            pick(v, t);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (row(t) + q < a.I && col(t) < a.J) store8v(part + (long)(row(t) + q) * a.J, v[q], col(t), a.J);
         }
     } else if (j0 + BJ <= a.J) {
-        // x_scale by way of LDS: loaded in the loop, it would wait for the
-        // stores there; applied to the accumulators, it would double them
-        if (F8) {
-#pragma unroll
-            for (int k = 0; k < NI; ++k)
-                if (g == 0) scales[16 * k + r] = ep.xs[min(i0 + wi + 16 * k + r, a.I - 1)];
-        }
-        const Epilogue::Cols c = ep.cols(j, a.J);
-        if (ep.residual) rows(std::true_type{}, c);
-        else rows(std::false_type{}, c);
+        if (ep.residual) turns(std::true_type{});
+        else turns(std::false_type{});
     } else {
 #pragma unroll 1
-        for (int y = 0; y < NI; ++y) {
-            put(y);
-#pragma unroll 1
-            for (int q = 0; q < Q; ++q) {
-                const int i = ib + 16 * y + q * RPP;
-                const f32x8 v = get(q);
-                if (i < a.I && j < a.J) ep.any(v, i, j, a.J);
-            }
+        for (int t = 0; t < TURNS; ++t) {
+            f32x8 v[2];
+            pick(v, t);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (row(t) + q < a.I && col(t) < a.J) ep.any(v[q], row(t) + q, col(t), a.J);
         }
     }
     if (AHEAD) mm_wait<0>();  // nothing may reach LDS after the workgroup's end
@@ -588,7 +607,7 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
 
 // Grid: x = tiles, y = splits of k.
 template <int BI, int BJ, int WI, int WJ, int NBUF, bool TV, bool TU, int MODE>
-__global__ __launch_bounds__(WI *WJ * 64) void mm_kernel(MmArgs a, Epilogue ep, float *part) {
+__global__ __launch_bounds__(WI *WJ * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void mm_kernel(MmArgs a, Epilogue ep, float *part) {
     __shared__ __attribute__((aligned(1024))) char smem[mm_lds<BI, BJ, WI, WJ, NBUF>()];
     mm_body<BI, BJ, WI, WJ, NBUF, TV, TU, MODE>(smem, a, ep, part, blockIdx.x, blockIdx.y);
 }
@@ -622,7 +641,7 @@ __device__ __forceinline__ void colsum_body(char *smem, const ColSums &c, int gr
 // together: workgroups 0 .. na - 1 are dx's tiles and splits, the next nb dw's,
 // those after them add up dbias.
 template <int NBUF>
-__global__ __launch_bounds__(256) void mm_pair_kernel(MmArgs a, Epilogue ea, float *pa, int na, MmArgs b, Epilogue eb,
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void mm_pair_kernel(MmArgs a, Epilogue ea, float *pa, int na, MmArgs b, Epilogue eb,
                                                       float *pb, int nb, ColSums c) {
     __shared__ __attribute__((aligned(1024))) char smem[mm_lds<128, 128, 2, 2, NBUF>()];
     const int g = blockIdx.x, ta = a.ti * a.tj, tb = b.ti * b.tj;
