@@ -919,22 +919,32 @@ static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, cons
         GDN_MV(1, 2, 8, 256);
         return hipGetLastError();
     }
-    // Up to 512 workgroups of 16 columns run in one or two rounds; more columns
-    // go 32 to a workgroup, which reads x half as often (17 x 16384 x 1024 in
-    // bf16: 8.8 against 13.5 us; 17 x 4096 x 4096: 10.2 against 15.9 the other
-    // way round).  One row tile's pieces are 256 bytes, which leaves room for
-    // two workgroups in a compute unit; rows of 16 KB and more bring 512 at a
-    // time (1 x 4096 x 16384: 30.9 against 34.2 us; 1 x 16384 x 1024: 9.1
-    // against 12.6 the other way round).
-    const bool wide = N > 512 * 16;
+    // 16 columns a workgroup, one of these in each compute unit with its LDS
+    // full of pieces in flight.  More columns than that (more) go to
+    // workgroups of fewer waves, three of which share a compute unit instead
+    // of taking turns (17 rows in e4m3: 4099 x 4096 8.3 against 9.3 us, 8192 x
+    // 1024 5.0 against 6.8; 4096 x 4096 8.4 against 6.9 the other way round),
+    // and beyond 512 workgroups (wide) 32 to one, which reads x half as often
+    // (17 x 16384 x 1024 in bf16: 8.1 against 9.4 us; 17 x 4096 x 4096: 15.9
+    // against 9.7 the other way round).  Up to 16 rows take so little LDS that
+    // two workgroups of eight waves share a compute unit; rows of 16 KB and
+    // more bring pieces of 512 bytes (1 x 4096 x 16384: 30.9 against 34.2 us;
+    // 1 x 16384 x 1024: 9.1 against 12.6 the other way round), and rows of 2 KB,
+    // which eight waves read in one turn, go to four (1 x 32768 x 1024 in bf16:
+    // 13.9 against 16.5 us; 1 x 32768 x 4096: 50.6 against 46.9 the other way round).
+    const bool wide = N > 512 * 16, more = N > kCUs * 16;
+    const long row = (long)K * (F8 ? 1 : 2);
     if (M <= 16) {
-        if ((long)K * (F8 ? 1 : 2) >= 16384 && !wide) GDN_MV(1, 1, 8, 512);
+        if (row >= 16384 && !wide) GDN_MV(1, 1, 8, 512);
+        else if (row <= 2048 && more) GDN_MV(1, 1, 4, 256);
         else GDN_MV(1, 1, 8, 256);
     } else if (M <= 32) {
         if (wide) GDN_MV(2, 2, 4, 256);
+        else if (more) GDN_MV(1, 2, 4, 256);
         else GDN_MV(1, 2, 8, 256);
     } else {
-        if (wide) GDN_MV(2, 4, 4, 256);
+        if (wide) GDN_MV(2, 4, 3, 256);
+        else if (more) GDN_MV(1, 4, 3, 256);
         else GDN_MV(1, 4, 7, 256);
     }
 #undef GDN_MV

@@ -290,6 +290,20 @@ def test_two_streams_at_once():
             assert torch.equal(a, y) and all(torch.equal(u, v) for u, v in zip(b, grads))
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 4105, 64), (5, 8203, 1024), (16, 9001, 2064), (30, 4105, 1040), (30, 8203, 528),
+                                   (50, 4105, 1040), (50, 8203, 528), (64, 8192, 1024), (3, 70, 16400)])
+def test_few_rows_of_many_columns(M, N, K):
+    """Each cut of the kernel for few rows, with whole and partial last pieces, exactly."""
+    rng = np.random.default_rng(28)
+    x, w = _ints(rng, (M, K), 3, BF), _ints(rng, (N, K), 3, BF)
+    want = _h(x) @ _h(w).T
+    assert np.array_equal(_h(gdn.gdn_linear(x, w, out_dtype=F32)[0]), want)
+    if K % 16 == 0:
+        one = lambda n: torch.ones(n, device="cuda")
+        y, _ = gdn.gdn_linear(x.to(F8), w.to(F8), x_scale=one(M), w_scale=one(N), out_dtype=F32)
+        assert np.array_equal(_h(y), want)
+
+
 @pytest.mark.parametrize("M,N", [(1_100_003, 2056), (2056, 1_100_003)])
 def test_offsets_past_2_to_the_31(M, N):
     """Outputs of 2.26e9 values: the corners against the same rows and columns computed alone."""
