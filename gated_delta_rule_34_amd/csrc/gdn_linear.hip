@@ -807,6 +807,8 @@ __device__ __forceinline__ float rest(float d, float hi) { return fabsf(hi) < __
 // dz = dy act'(z) in `planes` bf16 planes (rounded; what is left of it; what
 // is left of that) of Jp columns, Jp a multiple of 8, zero past J; and the
 // column sums of the unrounded dz over this workgroup's rows.
+// Bound by HBM: 16384 x 4096 with SiLU 85 us, 4.7 TB/s (97 with a row's loads
+// awaited before the next one's).
 template <class DT>
 __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z, uint16_t *out, long plane,
                                                  int planes, float *part, int I, int J, int Jp, int act, int rows) {
@@ -814,30 +816,40 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int j = (blockIdx.x * 64 + lane) * 8;
     const int i0 = blockIdx.y * rows, i1 = min(i0 + rows, I);
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    constexpr int AT = 4;  // rows requested together
+    f32x8 sum = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (j < Jp) {
-#pragma unroll 4
-        for (int i = i0 + wave; i < i1; i += 4) {
-            float d[8];
-            load_piece(d, dy + (long)i * J, j, J);
-            if (z) {
-                float t[8];
-                load_piece(t, z + (long)i * J, j, J);
+        for (int i = i0 + wave; i < i1; i += 4 * AT) {
+            typename RawOf<DT>::type rd[AT];
+            Raw16 rz[AT];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= act_bwd(act, t[e]);
+            for (int q = 0; q < AT; ++q) rd[q] = load_raw(dy + (long)min(i + 4 * q, i1 - 1) * J, j, J);
+            if (z) {
+#pragma unroll
+                for (int q = 0; q < AT; ++q) rz[q] = load_raw(z + (long)min(i + 4 * q, i1 - 1) * J, j, J);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += d[e];
-            if (out) {
-                for (int p = 0; p < planes; ++p) {
-                    u32x4 u;
+            for (int q = 0; q < AT; ++q) {
+                if (i + 4 * q >= i1) break;
+                f32x8 d = raw_f32(rd[q]);
+                if (z) {
+                    const f32x8 t = raw_f32(rz[q]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        u[e] = pack2_bf16(d[2 * e], d[2 * e + 1]);
-                        d[2 * e] = rest(d[2 * e], __uint_as_float(u[e] << 16));
-                        d[2 * e + 1] = rest(d[2 * e + 1], __uint_as_float(u[e] & 0xffff0000u));
+                    for (int e = 0; e < 8; ++e) d[e] *= act_bwd(act, t[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += d[e];
+                if (out) {
+                    for (int p = 0; p < planes; ++p) {
+                        u32x4 u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            u[e] = pack2_bf16(d[2 * e], d[2 * e + 1]);
+                            d[2 * e] = rest(d[2 * e], __uint_as_float(u[e] << 16));
+                            d[2 * e + 1] = rest(d[2 * e + 1], __uint_as_float(u[e] & 0xffff0000u));
+                        }
+                        *(u32x4 *)(out + p * plane + (long)(i + 4 * q) * Jp + j) = u;
                     }
-                    *(u32x4 *)(out + p * plane + (long)i * Jp + j) = u;
                 }
             }
         }
@@ -849,7 +861,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
     if (wave == 0 && j < J) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = ((sh[0][lane][e] + sh[1][lane][e]) + sh[2][lane][e]) + sh[3][lane][e];
-        store_piece(part + (long)blockIdx.y * J, sum, j, J);
+        store8v(part + (long)blockIdx.y * J, sum, j, J);
     }
 }
 
