@@ -280,6 +280,7 @@ static RowPlan bwd_plan(int D) {
     if (D <= 1024) return {64, 2};
     if (D <= 2048) return {256, 1};
     if (D <= 4096) return {256, 2};
+    if (D <= 6144) return {256, 3};  // fewer lanes past the row's end: 16384 x 5120 in fp32 189 against 214 us
     if (D <= 8192) return {512, 2};
     if (D <= 16384) return {512, 4};
     return {1024, 4};
@@ -288,15 +289,16 @@ static RowPlan bwd_plan(int D) {
 // Workgroups of the backward: enough to fill the card, few enough that their
 // partial sums stay small beside the rows.  Measured best counts over 64 to
 // 2048: 768 of four waves with a row each (32768 x 1024 in bf16: 39.6 us; 256
-// 50, 2048 46), 512 at 4096 columns (4096 rows: 23.8 us); beyond that one per
-// compute unit, two once there are rows for 16 each (777 x 5125 in fp32: 21.4
-// us at 256, 25.7 at 384; 5000 x 5000 in bf16: 45.6 us at 512, 60.2 at 256).
+// 50, 2048 46), 512, two per compute unit, up to 6144 columns (4096 x 4096
+// 22 us; 16384 x 5120 in fp32 189 us, 640 255, 260 292); beyond that one per
+// compute unit, two once there are rows for 16 each (5000 x 8000 in bf16 55
+// against 66 us, 16384 x 8192 151 against 148, fp32 106 against 103).
 int norm_bwd_blocks(long rows, int D) {
     const RowPlan p = bwd_plan(D);
     const int rpb = p.tpr < 256 ? 256 / p.tpr : 1;
     const long groups = (rows + rpb - 1) / rpb;
     const long wide = D <= 8192 && rows >= 4096 ? 512 : 256;
-    const long most = D <= 512 ? 1024 : D <= 2048 ? 768 : D <= 4096 ? 512 : wide;
+    const long most = D <= 512 ? 1024 : D <= 2048 ? 768 : D <= 6144 ? 512 : wide;
     return (int)(groups < most ? groups : most);
 }
 
@@ -317,6 +319,7 @@ static hipError_t launch_norm_bwd_t(const void *dy, const void *r, const float *
     GDN_NORMB(64, 2)
     GDN_NORMB(256, 1)
     GDN_NORMB(256, 2)
+    GDN_NORMB(256, 3)
     GDN_NORMB(512, 2)
     GDN_NORMB(512, 4)
     GDN_NORMB(1024, 4)

@@ -133,7 +133,7 @@ def test_in_place_and_rows_behind(D):
 
 @pytest.mark.parametrize("xd,rd", TYPES)
 @pytest.mark.parametrize("rows,D", [(1, 1), (3, 65), (700, 512), (37, 1024), (5, 2047), (1030, 2048), (9, 4096), (3, 8192),
-                                    (4, 16384), (2, 32767), (1500, 8)])
+                                    (4, 16384), (2, 32767), (1500, 8), (600, 5125), (3, 6143)])
 def test_norm_bwd(rows, D, xd, rd):
     rng = np.random.default_rng(rows + D)
     dy, r, dr = _t(rng, (rows, D), xd), _t(rng, (rows, D), rd, 2.0), _t(rng, (rows, D), rd)
