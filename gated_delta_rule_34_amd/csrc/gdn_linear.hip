@@ -1067,7 +1067,8 @@ LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, i
     const bool direct = !dy_f32 && act == ACT_NONE;        // dz is dy
     p.Np = (N + 7) / 8 * 8;
     p.copy = (dx || dw) && !(direct && p.Np == N);
-    p.planes = direct || !grad_f32 ? 1 : 3;
+    const bool exact = !dy_f32 && act <= ACT_RELU;         // dz is dy or zero: bf16 holds it
+    p.planes = exact || !grad_f32 ? 1 : 3;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     p.plane = up((size_t)M * p.Np * 2);
     size_t off = p.copy ? p.plane * p.planes : 0;

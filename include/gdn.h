@@ -479,9 +479,11 @@ gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const 
  *   dbias [N] fp32, nullable
  * dz takes part in the products as a bf16 operand.  With GDN_BF16 gradients
  * it is rounded to bf16 (as its products' results are); with GDN_F32 it is
- * kept exactly: dy itself where that is bf16 and there is no activation,
- * otherwise as three bf16 parts that together carry its fp32 value (three
- * times the products).  dbias sums the unrounded dz in a fixed order.
+ * kept exactly: in one part where dy is bf16 and the activation none or
+ * GDN_ACT_RELU (dz is dy or zero), otherwise as three bf16 parts that together
+ * carry its fp32 value (three times the products; an infinity in w or x meets
+ * parts that are zero and gives NaN).  dbias sums the unrounded dz in a fixed
+ * order.
  *   ws  gdn_linear_bwd_workspace() bytes (same sizes, types, activation and
  *       set of outputs), 256-byte aligned (may be NULL if 0)
  * Sizes as gdn_linear, with M * N limits for M * K and N * K too.  Errors as
