@@ -71,20 +71,21 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
     return z;
 }
 
-__device__ __forceinline__ float act_bwd(int act, float z) {
+// dy act'(z)
+__device__ __forceinline__ float dz_of(int act, float dy, float z) {
     switch (act) {
-        case ACT_RELU: return z > 0.f ? 1.f : 0.f;
+        case ACT_RELU: return z > 0.f ? dy : 0.f;  // a choice: 0 times an infinity would be NaN
         case ACT_SILU: {
             const float p = sigmoid_fast(z);
-            return p * (1.f + z * (1.f - p));
+            return dy * (p * (1.f + z * (1.f - p)));
         }
         case ACT_GELU: {
             float e;
             const float c = normal_cdf<true>(z, e);
-            return c + z * e * 0.3989422804014327f;
+            return dy * (c + z * e * 0.3989422804014327f);
         }
     }
-    return 1.f;
+    return dy;
 }
 
 // The epilogue of eight consecutive columns of one row.
@@ -864,7 +865,7 @@ __global__ __launch_bounds__(256) void dz_kernel(const DT *dy, const uint16_t *z
                 if (z) {
                     const f32x8 t = raw_f32(rz[q]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] *= act_bwd(act, t[e]);
+                    for (int e = 0; e < 8; ++e) d[e] = dz_of(act, d[e], t[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += d[e];

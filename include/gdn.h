@@ -473,6 +473,8 @@ gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const 
  * gdn_linear_bwd -- gradients of gdn_linear with bf16 x and w, for
  * L = sum(dy . y) (the gradient of residual is dy itself):
  *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum over rows of dz
+ * (GDN_ACT_RELU chooses: dz is dy where z > 0 and 0 elsewhere, whatever dy
+ * holds there)
  *   dy [M, N] dy_dtype (GDN_BF16 or GDN_F32), 16-byte aligned
  *   z  [M, N] bf16, 16-byte aligned: required with an activation, null without
  *   dx [M, K], dw [N, K]  grad_dtype (GDN_BF16 or GDN_F32), 16-byte aligned, nullable

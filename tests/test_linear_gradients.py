@@ -57,3 +57,17 @@ def test_an_infinite_weight_meets_no_parts_of_zero():
     rest = [c for c in range(K) if c != 7]
     np.testing.assert_array_equal(_h(dx[:, rest]), np.broadcast_to(_h(w[:, rest]).sum(0), (M, K - 1)))
     np.testing.assert_array_equal(_h(dw), np.broadcast_to(_h(x).sum(0), (N, K)))
+
+
+@gpu
+@pytest.mark.parametrize("dyt,grad", [(BF, BF), (BF, F32), (F32, F32)])
+def test_relu_hides_what_it_masks(dyt, grad):
+    """Where z <= 0 nothing of dy comes through, an infinity or NaN neither."""
+    rng = np.random.default_rng(6)
+    M, N, K = 70, 136, 64
+    x, w, dy, z = _ints(rng, (M, K), 3, BF), _ints(rng, (N, K), 3, BF), _ints(rng, (M, N), 3, dyt), _ints(rng, (M, N), 2, BF)
+    z[5, 9], z[6, 130], z[69, 0] = 0.0, -1.0, -2.0
+    want = gdn.gdn_linear_bwd(dy, x, w, z=z, act="relu", bias=True, grad_dtype=grad)
+    dy[5, 9], dy[6, 130], dy[69, 0] = float("nan"), float("inf"), -float("inf")
+    got = gdn.gdn_linear_bwd(dy, x, w, z=z, act="relu", bias=True, grad_dtype=grad)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
