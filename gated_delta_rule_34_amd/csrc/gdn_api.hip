@@ -680,23 +680,24 @@ gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long row
 }
 
 // Sizes of a product the kernels index: 32-bit offsets within a tile of 256
-// rows, a grid of fewer than 2^32 threads.
-static bool mm_sizes_ok(int M, int N, int K) {
+// rows (N, K), a grid of fewer than 2^32 threads (the tiles of each output:
+// M x N in the forward, M x K and N x K in the backward, which reads M x N).
+static bool mm_sizes_ok(int M, int N, int K, bool bwd) {
     auto tiles = [](long long a, long long b) { return ((a + 255) / 256) * ((b + 255) / 256) < (1LL << 21); };
-    return N <= (1 << 22) && K <= (1 << 22) && tiles(M, N) && tiles(M, K) && tiles(N, K);
+    return N <= (1 << 22) && K <= (1 << 22) && tiles(M, N) && (!bwd || (tiles(M, K) && tiles(N, K)));
 }
 
 static bool act_ok(gdn_act a) { return a >= GDN_ACT_NONE && a <= GDN_ACT_GELU; }
 
-static gdn_status linear_check(int M, int N, int K, gdn_dtype dtype) {
+static gdn_status linear_check(int M, int N, int K, gdn_dtype dtype, bool bwd) {
     if (M < 1 || N < 1 || K < 1) return GDN_ERR_INVALID_ARG;
     if (dtype != GDN_BF16 && dtype != GDN_F8E4M3) return GDN_ERR_UNSUPPORTED;
-    if (K % (dtype == GDN_BF16 ? 8 : 16) || !mm_sizes_ok(M, N, K)) return GDN_ERR_UNSUPPORTED;
+    if (K % (dtype == GDN_BF16 ? 8 : 16) || !mm_sizes_ok(M, N, K, bwd)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
 size_t gdn_linear_workspace(int M, int N, int K, gdn_dtype dtype) {
-    if (linear_check(M, N, K, dtype) != GDN_OK) return 0;
+    if (linear_check(M, N, K, dtype, false) != GDN_OK) return 0;
     return align_up(gdn::linear_ws_bytes(gdn::linear_plan(M, N, K, dtype == GDN_F8E4M3), M, N));
 }
 
@@ -704,7 +705,7 @@ gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const 
                       const void *residual, void *y, void *z, int M, int N, int K, gdn_dtype dtype,
                       gdn_dtype out_dtype, gdn_act act, void *ws, size_t ws_bytes, void *stream) {
     if (!x || !w || !y) return GDN_ERR_INVALID_ARG;
-    const gdn_status st = linear_check(M, N, K, dtype);
+    const gdn_status st = linear_check(M, N, K, dtype, false);
     if (st != GDN_OK) return st;
     if (!dtype_ok(out_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
     const bool f8 = dtype == GDN_F8E4M3;
@@ -727,7 +728,7 @@ gdn_status gdn_linear(const void *x, const void *w, const float *x_scale, const 
 
 size_t gdn_linear_bwd_workspace(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
                                 int need_dx, int need_dw, int need_dbias) {
-    if (linear_check(M, N, K, GDN_BF16) != GDN_OK || !dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act))
+    if (linear_check(M, N, K, GDN_BF16, true) != GDN_OK || !dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act))
         return 0;
     return gdn::linear_bwd_plan(M, N, K, dy_dtype == GDN_F32, grad_dtype == GDN_F32, (int)act, need_dx != 0,
                                 need_dw != 0, need_dbias != 0)
@@ -738,7 +739,7 @@ gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const vo
                           float *dbias, int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
                           void *ws, size_t ws_bytes, void *stream) {
     if (!dy || !x || !w || (!dx && !dw && !dbias)) return GDN_ERR_INVALID_ARG;
-    const gdn_status st = linear_check(M, N, K, GDN_BF16);
+    const gdn_status st = linear_check(M, N, K, GDN_BF16, true);
     if (st != GDN_OK) return st;
     if (!dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
     if ((act != GDN_ACT_NONE) != (z != nullptr)) return GDN_ERR_INVALID_ARG;
