@@ -20,6 +20,7 @@ __all__ = [
     "gdn2_chunk_bwd", "gdn2_chunk_bwd_workspace", "gdn2_chunk_fwd_noalloc", "gdn2_chunk_fwd_noalloc_max_bytes",
     "gdn_add_rmsnorm", "gdn_add_rmsnorm_bwd", "gdn_add_rmsnorm_bwd_workspace", "gdn_quantize_rows",
     "gdn_linear", "gdn_linear_workspace", "gdn_linear_bwd", "gdn_linear_bwd_workspace",
+    "gdn_linear_plan", "gdn_linear_bwd_plan",
     "clock_probe",
     "GDN_F32", "GDN_BF16", "GDN_F8E4M3", "BT",
 ]
@@ -102,6 +103,10 @@ def load():
     lib.gdn_linear.argtypes = [_vp] * 8 + [_i] * 6 + [_vp, _sz, _vp]
     lib.gdn_linear_bwd_workspace.restype = _sz
     lib.gdn_linear_bwd_workspace.argtypes = [_i] * 9
+    lib.gdn_linear_plan.restype = _i
+    lib.gdn_linear_plan.argtypes = [_i] * 4 + [_vp]
+    lib.gdn_linear_bwd_plan.restype = _i
+    lib.gdn_linear_bwd_plan.argtypes = [_i] * 9 + [_vp]
     lib.gdn_linear_bwd.restype = _i
     lib.gdn_linear_bwd.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
     _lib = lib
@@ -870,6 +875,26 @@ def gdn_linear_bwd(dy, x, weight, z=None, act="none", bias=False, grad_dtype=Non
                _addr(dy), _addr(x), _addr(weight), _addr(z) if a else None, _addr(dx), _addr(dw), _addr(db), M, N, K,
                dyc, gc, a, _addr(ws), nbytes)
     return dx, dw, db
+
+
+_CUT = ("tile", "splits", "slabs", "buffers")
+
+
+def gdn_linear_plan(M, N, K, dtype_code):
+    """How gdn_linear cuts a product (measurement and test aid): {"tile": edge of the output tiles, 0 for the kernel
+    of few rows or columns, "splits": parts of k, "slabs": slabs of 128 bytes of k in each, "buffers": of a slab}."""
+    plan = (ctypes.c_int * 4)()
+    _check(load().gdn_linear_plan(M, N, K, dtype_code, plan), "gdn_linear_plan")
+    return dict(zip(_CUT, plan))
+
+
+def gdn_linear_bwd_plan(M, N, K, dy_code, grad_code, act, need_dx=True, need_dw=True, need_dbias=False):
+    """The same of gdn_linear_bwd: {"parts": bf16 parts of dz, "pair": slab buffers of the launch that dx and dw share
+    or 0, "dx": and "dw": their cuts}."""
+    plan = (ctypes.c_int * 10)()
+    _check(load().gdn_linear_bwd_plan(M, N, K, dy_code, grad_code, _act_code(act), int(need_dx), int(need_dw),
+                                      int(need_dbias), plan), "gdn_linear_bwd_plan")
+    return {"parts": plan[0], "pair": plan[1], "dx": dict(zip(_CUT, plan[2:6])), "dw": dict(zip(_CUT, plan[6:10]))}
 
 
 def clock_probe(nblocks=256, spin_us=2000, device="cuda"):

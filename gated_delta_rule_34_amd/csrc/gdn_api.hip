@@ -759,4 +759,34 @@ gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const vo
                                            grad_dtype == GDN_F32, (int)act, (char *)ws, (hipStream_t)stream));
 }
 
+static void plan_ints(const gdn::MmPlan &p, int *out) {
+    out[0] = p.tile;
+    out[1] = p.splits;
+    out[2] = p.per_split;
+    out[3] = p.tile ? (p.deep ? 4 : 2) : 0;
+}
+
+gdn_status gdn_linear_plan(int M, int N, int K, gdn_dtype dtype, int *plan) {
+    if (!plan) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = linear_check(M, N, K, dtype, false);
+    if (st != GDN_OK) return st;
+    plan_ints(gdn::linear_plan(M, N, K, dtype == GDN_F8E4M3), plan);
+    return GDN_OK;
+}
+
+gdn_status gdn_linear_bwd_plan(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act, int need_dx,
+                               int need_dw, int need_dbias, int *plan) {
+    if (!plan) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = linear_check(M, N, K, GDN_BF16, true);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
+    const gdn::LinearBwdPlan p = gdn::linear_bwd_plan(M, N, K, dy_dtype == GDN_F32, grad_dtype == GDN_F32, (int)act,
+                                                      need_dx != 0, need_dw != 0, need_dbias != 0);
+    plan[0] = p.planes;
+    plan[1] = p.pair ? (p.deep ? 4 : 2) : 0;
+    plan_ints(p.dx, plan + 2);
+    plan_ints(p.dw, plan + 6);
+    return GDN_OK;
+}
+
 }  // extern "C"

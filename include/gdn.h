@@ -499,6 +499,21 @@ gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const vo
                           void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * gdn_linear_plan, gdn_linear_bwd_plan -- measurement and test aid, not part
+ * of the operation: how a call of these sizes is cut.  Host only.
+ *   plan (host) of the forward, 4 ints: edge of the output tiles (0: the
+ *     kernel for few rows or columns), parts that k is split in, slabs of 128
+ *     bytes of k in each, slab buffers
+ *   plan of the backward, 10 ints: bf16 parts of dz, slab buffers of the
+ *     launch that dx and dw share (0: a launch each), then the four ints of
+ *     dx and those of dw (zero where not asked for)
+ * Errors: GDN_ERR_INVALID_ARG (null plan, bad sizes), GDN_ERR_UNSUPPORTED.
+ */
+gdn_status gdn_linear_plan(int M, int N, int K, gdn_dtype dtype, int *plan);
+gdn_status gdn_linear_bwd_plan(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act, int need_dx,
+                               int need_dw, int need_dbias, int *plan);
+
+/*
  * gdn_clock_probe -- measurement aid, not part of the operation: enqueues
  * nblocks single-wave workgroups that each spin for spin_us microseconds of
  * real time and write two counts to out (device, 2 * nblocks uint64): the

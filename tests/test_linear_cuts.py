@@ -1,0 +1,139 @@
+"""Every way gdn_linear and gdn_linear_bwd cut a product into tiles, parts of k
+and slab buffers, in bf16 and e4m3, against exact whole-number results.
+
+A CPU test holds the lists of sizes to what they are there for: it asks the
+library how it cuts each of them."""
+import os
+
+import numpy as np
+import pytest
+
+import gated_delta_rule_34_amd as gdn
+
+torch = pytest.importorskip("torch")
+
+BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+gpu = pytest.mark.gpu
+built = pytest.mark.skipif(not os.path.exists(gdn.lib_path), reason="libgdn.so not built")
+
+# the tile's edge, slab buffers, whether k is split
+CUTS = {(256, 2, False), (256, 2, True), (128, 4, False), (128, 4, True), (128, 2, False), (128, 2, True)}
+FORWARD_F8 = [(2900, 2900, 1040), (256, 256, 8192), (100, 1000, 1040), (256, 1000, 4112), (1500, 2900, 1040),
+              (600, 1100, 16400)]
+FORWARD_BF16 = [(2900, 2900, 1040), (100, 1000, 1040), (333, 4096, 1032), (500, 250, 8200), (1500, 2900, 1040),
+                (600, 1100, 16400)]
+# (M, N, K, need_dx, need_dw); shared launches with two and with four buffers first
+BACKWARD = [(200, 515, 64, 1, 1), (3000, 515, 264, 1, 1), (4100, 515, 264, 1, 1), (600, 2100, 1024, 1, 1),
+            (2000, 515, 1024, 1, 1), (200, 1100, 2056, 1, 1),
+            (70, 515, 64, 1, 0), (1100, 4100, 64, 1, 0), (2000, 515, 2056, 1, 1), (2000, 4100, 64, 1, 1),
+            (4100, 515, 2056, 1, 1), (3000, 1100, 64, 1, 0),
+            (200, 24, 64, 0, 1), (3000, 515, 264, 0, 1), (200, 4100, 1024, 1, 1), (200, 4100, 2056, 1, 1),
+            (4100, 515, 64, 0, 1)]
+
+
+def _key(c):
+    return c["tile"], c["buffers"], c["splits"] > 1
+
+
+@built
+@pytest.mark.parametrize("sizes,code,per", [(FORWARD_F8, gdn.GDN_F8E4M3, 128), (FORWARD_BF16, gdn.GDN_BF16, 64)])
+def test_the_forward_sizes_reach_every_cut(sizes, code, per):
+    cuts = [gdn.gdn_linear_plan(*s, code) for s in sizes]
+    assert {_key(c) for c in cuts} == CUTS
+    for tile, buffers in ((256, 2), (128, 4), (128, 2)):
+        # beyond the filling of the buffers, with a ragged last slab
+        assert any(c["tile"] == tile and c["buffers"] == buffers and c["slabs"] > 2 * buffers and s[2] % per
+                   for c, s in zip(cuts, sizes))
+    few = gdn.gdn_linear_plan(64, 4096, 1024, code)
+    assert few["tile"] == 0 and few["splits"] == 1
+
+
+@built
+def test_the_backward_sizes_reach_every_cut():
+    alone, pair = {"dx": set(), "dw": set()}, {"dx": set(), "dw": set()}
+    for M, N, K, a, b in BACKWARD:
+        p = gdn.gdn_linear_bwd_plan(M, N, K, gdn.GDN_BF16, gdn.GDN_BF16, "none", a, b)
+        for w, asked in (("dx", a), ("dw", b)):
+            if not asked:
+                assert not p[w]["tile"]
+            elif p["pair"]:
+                assert p[w]["tile"] == 128
+                pair[w].add((p["pair"], p[w]["splits"] > 1))
+            else:
+                alone[w].add(_key(p[w]))
+    assert alone["dx"] == CUTS and alone["dw"] == CUTS
+    assert pair["dx"] >= {(4, False), (2, False), (2, True)}
+    assert pair["dw"] == {(4, False), (4, True), (2, False), (2, True)}
+
+
+@built
+def test_plans_refuse_what_the_calls_refuse():
+    for bad in ((0, 8, 8), (8, 8, 12), (8, (1 << 22) + 1, 8)):
+        with pytest.raises(RuntimeError):
+            gdn.gdn_linear_plan(*bad, gdn.GDN_BF16)
+        with pytest.raises(RuntimeError):
+            gdn.gdn_linear_bwd_plan(*bad, gdn.GDN_BF16, gdn.GDN_BF16, "none")
+    with pytest.raises(RuntimeError):
+        gdn.gdn_linear_plan(8, 8, 8, gdn.GDN_F32)
+    lib = gdn.load()
+    assert lib.gdn_linear_plan(8, 8, 8, gdn.GDN_BF16, None) == 1
+    assert lib.gdn_linear_bwd_plan(8, 8, 8, gdn.GDN_BF16, gdn.GDN_BF16, 0, 1, 1, 0, None) == 1
+
+
+def _ints(rng, shape, top, dt=BF):
+    return torch.from_numpy(rng.integers(-top, top + 1, shape).astype(np.float32)).to(dt).cuda()
+
+
+def _h(t):
+    return t.detach().float().cpu().double().numpy()
+
+
+def _rounded(ref):
+    return torch.from_numpy(ref).float().to(BF).double().numpy()
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", FORWARD_F8)
+def test_e4m3_exact(M, N, K):
+    """Whole numbers up to 3: products and sums are exact in fp32 in any order, and no product lies 13 bits below
+    another."""
+    rng = np.random.default_rng(M + N + K)
+    x, w = _ints(rng, (M, K), 3, F32).to(F8), _ints(rng, (N, K), 3, F32).to(F8)
+    xs = torch.from_numpy(2.0 ** rng.integers(-3, 4, M)).float().cuda()
+    ws = torch.from_numpy(2.0 ** rng.integers(-3, 4, N)).float().cuda()
+    b, res = _ints(rng, (N,), 9, F32), _ints(rng, (M, N), 9)
+    z = (_h(x) @ _h(w).T) * _h(xs)[:, None] * _h(ws)
+    y, _ = gdn.gdn_linear(x, w, x_scale=xs, w_scale=ws, out_dtype=F32)
+    np.testing.assert_array_equal(_h(y), z)
+    y, zz = gdn.gdn_linear(x, w, bias=b, x_scale=xs, w_scale=ws, act="relu", residual=res, return_preact=True)
+    np.testing.assert_array_equal(_h(zz), _rounded(z + _h(b)))
+    np.testing.assert_array_equal(_h(y), _rounded(np.maximum(z + _h(b), 0) + _h(res)))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", FORWARD_BF16)
+def test_bf16_exact(M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    x, w, b, res = _ints(rng, (M, K), 3), _ints(rng, (N, K), 3), _ints(rng, (N,), 9, F32), _ints(rng, (M, N), 9)
+    z = _h(x) @ _h(w).T + _h(b)
+    y, zz = gdn.gdn_linear(x, w, bias=b, act="relu", residual=res, return_preact=True)
+    np.testing.assert_array_equal(_h(zz), _rounded(z))
+    np.testing.assert_array_equal(_h(y), _rounded(np.maximum(z, 0) + _h(res)))
+    y, _ = gdn.gdn_linear(x, w, bias=b, out_dtype=F32)
+    np.testing.assert_array_equal(_h(y), z)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,need_dx,need_dw", BACKWARD)
+def test_backward_exact(M, N, K, need_dx, need_dw):
+    rng = np.random.default_rng(M + N + K)
+    x, w, dy = _ints(rng, (M, K), 3), _ints(rng, (N, K), 3), _ints(rng, (M, N), 3)
+    rx, rw, rb = _h(dy) @ _h(w), _h(dy).T @ _h(x), _h(dy).sum(0)
+    for grad, to in ((F32, lambda r: r), (BF, _rounded)):
+        dx, dw, db = gdn.gdn_linear_bwd(dy, x, w, bias=True, grad_dtype=grad, need_dx=bool(need_dx), need_dw=bool(need_dw))
+        np.testing.assert_array_equal(_h(db), rb)
+        for got, ref, asked in ((dx, rx, need_dx), (dw, rw, need_dw)):
+            if asked:
+                np.testing.assert_array_equal(_h(got), to(ref))
+            else:
+                assert got is None
