@@ -1,5 +1,6 @@
 """Every way gdn_linear and gdn_linear_bwd cut a product into tiles, parts of k
-and slab buffers, in bf16 and e4m3, against exact whole-number results.
+and slab buffers, in bf16 and e4m3, against exact whole-number results; and
+the places of the three parts of an fp32 dz in dw.
 
 A CPU test holds the lists of sizes to what they are there for: it asks the
 library how it cuts each of them."""
@@ -29,6 +30,8 @@ BACKWARD = [(200, 515, 64, 1, 1), (3000, 515, 264, 1, 1), (4100, 515, 264, 1, 1)
             (4100, 515, 2056, 1, 1), (3000, 1100, 64, 1, 0),
             (200, 24, 64, 0, 1), (3000, 515, 264, 0, 1), (200, 4100, 1024, 1, 1), (200, 4100, 2056, 1, 1),
             (4100, 515, 64, 0, 1)]
+# dw over three parts of dz whose splits of k cross from one part into the next
+THREE_PARTS = [(70, 130, 136), (300, 515, 264), (2000, 24, 64), (2000, 1100, 520)]
 
 
 def _key(c):
@@ -64,6 +67,16 @@ def test_the_backward_sizes_reach_every_cut():
     assert alone["dx"] == CUTS and alone["dw"] == CUTS
     assert pair["dx"] >= {(4, False), (2, False), (2, True)}
     assert pair["dw"] == {(4, False), (4, True), (2, False), (2, True)}
+
+
+@built
+def test_the_splits_of_three_parts_cross_them():
+    crossing = 0
+    for M, N, K in THREE_PARTS:
+        p = gdn.gdn_linear_bwd_plan(M, N, K, gdn.GDN_F32, gdn.GDN_F32, "relu", False, True)
+        assert p["parts"] == 3
+        crossing += p["dw"]["splits"] > 1 and -(-M // 64) % p["dw"]["slabs"] != 0
+    assert crossing >= 2
 
 
 @built
@@ -137,3 +150,23 @@ def test_backward_exact(M, N, K, need_dx, need_dw):
                 np.testing.assert_array_equal(_h(got), to(ref))
             else:
                 assert got is None
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", THREE_PARTS)
+def test_every_part_of_dz_has_its_place_in_dw(M, N, K):
+    """dy in fp32 with 23 significant bits, one number in each column at most and x of powers of two: every element of
+    dw is one exact product, which a lost or misplaced part would change."""
+    rng = np.random.default_rng(M + N)
+    x = (torch.exp2(_ints(rng, (M, K), 2, F32)) * torch.where(_ints(rng, (M, K), 1, F32) < 0, -1.0, 1.0)).to(BF)
+    w = _ints(rng, (N, K), 3)
+    z, dy = _ints(rng, (M, N), 2), torch.zeros(M, N, device="cuda")
+    row = torch.from_numpy(rng.integers(0, M, N)).cuda()
+    col = torch.arange(N, device="cuda")
+    top = (2.0 ** 22 + rng.integers(0, 2 ** 22, N)) * np.where(rng.random(N) < 0.5, -1.0, 1.0)
+    dy[row, col] = torch.from_numpy(top.astype(np.float32)).cuda()
+    z[row, col] = torch.from_numpy(np.where(rng.random(N) < 0.8, 1.0, -1.0).astype(np.float32)).to(BF).cuda()
+    dz = torch.where(z.float() > 0, dy, 0.0).double()
+    _, dw, db = gdn.gdn_linear_bwd(dy, x, w, z=z, act="relu", bias=True, grad_dtype=F32, need_dx=False)
+    assert torch.equal(db.double(), dz.sum(0))
+    assert torch.equal(dw.double(), dz[row, col][:, None] * x.double()[row])
