@@ -1,6 +1,7 @@
 """Every way gdn_linear and gdn_linear_bwd cut a product into tiles, parts of k
-and slab buffers, in bf16 and e4m3, against exact whole-number results; and
-the places of the three parts of an fp32 dz in dw.
+and slab buffers, in bf16 and e4m3, against exact whole-number results; the
+sums of e4m3 products on values that spread over the type's range; and the
+places of the three parts of an fp32 dz in dw.
 
 A CPU test holds the lists of sizes to what they are there for: it asks the
 library how it cuts each of them."""
@@ -150,6 +151,60 @@ def test_backward_exact(M, N, K, need_dx, need_dw):
                 np.testing.assert_array_equal(_h(got), to(ref))
             else:
                 assert got is None
+
+
+def _spread(rng, shape):
+    """e4m3 values over most of the type's range, subnormal ones among them."""
+    v = rng.standard_normal(shape) * 2.0 ** rng.integers(-8, 7, shape)
+    return torch.from_numpy(np.clip(v, -448, 448).astype(np.float32)).to(F8).cuda()
+
+
+def _exponent(t):
+    """floor(log2|t|), not below that of the smallest normal value."""
+    return torch.where(t.float() == 0, -6, torch.frexp(t.float())[1].clamp(min=-5) - 1)
+
+
+def _cut_off(x, w):
+    """What the e4m3 instructions may drop of each sum: they add products in groups of eight consecutive k, each cut
+    off at 2^-13 of 2^(ex + ew), the group's largest sum of exponents; seven of the eight lose something."""
+    ex, ew = _exponent(x), _exponent(w)
+    out = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device="cuda")
+    for k in range(0, x.shape[1], 8):
+        top = (ex[:, None, k:k + 8] + ew[None, :, k:k + 8]).amax(-1)
+        out += 7 * torch.exp2(top.double() - 13)
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(100, 1000, 4112), (300, 500, 16400), (1500, 700, 1040), (2900, 2900, 1040)])
+@pytest.mark.parametrize("cancel", [False, True])
+def test_e4m3_sums_of_spread_values(M, N, K, cancel):
+    """bf16 outputs: the cut-off, an fp32 rounding for each addition (K 2^-24 sum|x w| at most) and the output's own
+    (2^-8); fp32 outputs: no cut-off.  cancel: the second half of k repeats the first, negated and in another order, so
+    that sums come out near zero and nothing of an error hides under the output's rounding."""
+    rng = np.random.default_rng(M + K)
+    if cancel:
+        h = K // 2
+        order = torch.from_numpy(rng.permutation(h)).cuda()
+        x, w = _spread(rng, (M, h)), _spread(rng, (N, h))
+        x = torch.cat([x, x.view(torch.uint8)[:, order].view(F8)], 1)
+        w = torch.cat([w, (-w.float()[:, order]).to(F8)], 1)
+    else:
+        x, w = _spread(rng, (M, K)), _spread(rng, (N, K))
+    xs = torch.from_numpy(2.0 ** rng.integers(-3, 4, M)).float().cuda()
+    ws = torch.from_numpy(2.0 ** rng.integers(-3, 4, N)).float().cuda()
+    s = xs.double()[:, None] * ws.double()
+    ref = (x.double() @ w.double().t().contiguous()) * s
+    size = (x.double().abs() @ w.double().abs().t().contiguous()) * s
+    y, z = gdn.gdn_linear(x, w, x_scale=xs, w_scale=ws, out_dtype=F32, return_preact=True)
+    err = (y.double() - ref).abs()
+    assert bool((err <= K * 2.0 ** -24 * size).all()), f"fp32: {float((err / size).max()):.2e} of sum|x w|"
+    assert torch.equal(z, y.to(BF))
+    y, z = gdn.gdn_linear(x, w, x_scale=xs, w_scale=ws, return_preact=True)
+    assert torch.equal(y, z)
+    err = (y.double() - ref).abs()
+    bar = (1 + 2.0 ** -8) * (_cut_off(x, w) * s + K * 2.0 ** -24 * size) + 2.0 ** -8 * ref.abs()
+    assert bool((err <= bar).all()), f"bf16: {float((err / bar).max()):.2f} of the bar"
 
 
 @gpu
