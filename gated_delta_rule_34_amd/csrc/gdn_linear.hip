@@ -547,8 +547,12 @@ __device__ __forceinline__ void mm_body(char *smem, const MmArgs &a, const Epilo
         // they are no longer than 2 KB, on the way: one touch a cache line,
         // shared among the workgroups that will use them.  They arrive during
         // the epilogue; left to the next tile's own loads, which all miss at
-        // once when a band begins, such a tile took 35 us for 27 (32768 x
-        // 4096 x 1024 in bf16: 268 -> 260 us).
+        // once when a band begins, such a tile took 35 us for 27.  32768 x 4096
+        // x 1024 in bf16 with x from HBM: 257 against 268 us, to fp32 300
+        // against 311, K = 512 166 against 173, e4m3 with K = 2048 258 against
+        // 268, with SiLU and pre-activation 311 both; it costs where x is in
+        // the caches already (244 against 238, with SiLU 290 against 273), and
+        // with rows of 4 KB (32768 x 1024 x 2048: 112 against 104 us).
         if (a.ldv <= 2048 && tile + kCUs < a.ti * a.tj) {
             int ni, nj;
             mm_tile(tile + kCUs, a.ti, a.tj, ni, nj);
@@ -979,22 +983,31 @@ static hipError_t mv_run(const void *x, const void *w, int M, int N, int K, cons
     // workgroups of fewer waves, three of which share a compute unit instead
     // of taking turns (17 rows in e4m3: 4099 x 4096 8.3 against 9.3 us, 8192 x
     // 1024 5.0 against 6.8; 4096 x 4096 8.4 against 6.9 the other way round),
-    // and beyond 512 workgroups (wide) 32 to one, which reads x half as often
-    // (17 x 16384 x 1024 in bf16: 8.1 against 9.4 us; 17 x 4096 x 4096: 15.9
-    // against 9.7 the other way round).  Up to 16 rows take so little LDS that
-    // two workgroups of eight waves share a compute unit; rows of 16 KB and
-    // more bring pieces of 512 bytes (1 x 4096 x 16384: 30.9 against 34.2 us;
-    // 1 x 16384 x 1024: 9.1 against 12.6 the other way round), and rows of 2 KB,
-    // which eight waves read in one turn, go to four (1 x 32768 x 1024 in bf16:
-    // 13.9 against 16.5 us; 1 x 32768 x 4096: 50.6 against 46.9 the other way round).
-    const bool wide = N > 512 * 16, more = N > kCUs * 16;
+    // and beyond what the card holds of these at once (wide: two to a compute
+    // unit for 33 rows and more, three below) 32 to one, which reads x half as
+    // often (17 x 16384 x 1024 in bf16: 8.1 against 9.4 us; 17 x 4096 x 4096:
+    // 15.9 against 9.7 the other way round; at the bounds, bf16: 64 x 8208 x
+    // 4096 29.4 against 35.9 us, x 8192 25.8 against 25.3; 20 x 12304 x 8192
+    // 48.8 against 50.0, x 12288 50.5 against 45.9).  Up to 16 rows take so
+    // little LDS that two workgroups of eight waves share a compute unit.
+    // There rows of 16 KB and more bring pieces of 512 bytes for up to four
+    // rows of x (1 x 1024 x 16384 in bf16: 13.3 against 15.5 us, x 24576 20.1
+    // against 22.6; 4 x 4096 x 8192 17.0 both; more rows lose: 16 x 4096 x 8192
+    // 18.8 against 17.1, x 20480 39.1 against 36.8) and, where the rows lie a
+    // multiple of 32 KB apart, on the same memory channels, for all (8 x 4096 x
+    // 16384 30.1 against 35.7 us, 16 rows 31.9 against 35.3); beyond 8192
+    // columns they gain nothing (1 x 8192 x 16384: 62.4 against 61.6).  Rows of
+    // 2 KB, which eight waves read in one turn, go to four (1 x 32768 x 1024 in
+    // bf16: 13.8 against 16.3 us, x 8192 5.4 against 5.6; 1 x 16384 x 2048: 16.8
+    // against 15.5 the other way round).
+    const bool wide = N > 2 * kCUs * 16, more = N > kCUs * 16;
     const long row = (long)K * (F8 ? 1 : 2);
     if (M <= 16) {
-        if (row >= 16384 && !wide) GDN_MV(1, 1, 8, 512);
+        if (row >= 16384 && !wide && (M <= 4 || row % 32768 == 0)) GDN_MV(1, 1, 8, 512);
         else if (row <= 2048 && more) GDN_MV(1, 1, 4, 256);
         else GDN_MV(1, 1, 8, 256);
     } else if (M <= 32) {
-        if (wide) GDN_MV(2, 2, 4, 256);
+        if (N > 3 * kCUs * 16) GDN_MV(2, 2, 4, 256);
         else if (more) GDN_MV(1, 2, 4, 256);
         else GDN_MV(1, 2, 8, 256);
     } else {

@@ -137,6 +137,28 @@ def test_bf16_exact(M, N, K):
     np.testing.assert_array_equal(_h(y), z)
 
 
+# each cut of the kernel for few rows, with whole and partial last pieces
+FEW_ROWS = [(3, 70, 8208), (4, 8192, 8192), (9, 70, 16384), (16, 33, 32768), (9, 70, 16400), (16, 4097, 8208), (5, 8203, 1024),
+            (20, 4096, 1040), (32, 12288, 528), (20, 12289, 528), (32, 12305, 2064), (33, 4096, 528), (50, 8192, 1040),
+            (64, 8193, 528)]
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", FEW_ROWS)
+def test_few_rows_exact(M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    x, w, res = _ints(rng, (M, K), 3), _ints(rng, (N, K), 3), _ints(rng, (M, N), 9)
+    ref = _h(x) @ _h(w).T
+    assert gdn.gdn_linear_plan(M, N, K, gdn.GDN_BF16)["tile"] == 0
+    np.testing.assert_array_equal(_h(gdn.gdn_linear(x, w, out_dtype=F32)[0]), ref)
+    np.testing.assert_array_equal(_h(gdn.gdn_linear(x, w, residual=res)[0]), _rounded(ref + _h(res)))
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    for twice in (1, 2):    # rows of as many bytes as in bf16, too
+        x8, w8 = (torch.cat([t.float().to(F8)] * twice, 1) for t in (x, w))
+        y, _ = gdn.gdn_linear(x8, w8, x_scale=one(M), w_scale=one(N), out_dtype=F32)
+        np.testing.assert_array_equal(_h(y), twice * ref)
+
+
 @gpu
 @pytest.mark.parametrize("M,N,K,need_dx,need_dw", BACKWARD)
 def test_backward_exact(M, N, K, need_dx, need_dw):
