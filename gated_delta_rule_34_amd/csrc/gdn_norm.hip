@@ -10,12 +10,13 @@
 // norm is taken of the unrounded sum u, so y does not depend on the type the
 // residual stream is kept in.  The kernels are bound by HBM: a row is read
 // once, held in registers while its sums are formed, and written once.  A row
-// belongs to one wave up to 2048 columns (four rows per workgroup, sums on
-// DPP with no LDS), beyond that to 256, 512 or 1024 threads with one LDS
-// exchange per sum.  Columns go in pieces of eight per lane; rows of a width
-// that is no multiple of eight start at any element, so the 16-byte accesses
-// are declared with element alignment (the hardware takes them at any
-// address) and the row's last few columns go one by one.
+// belongs to one wave up to 2048 columns in the forward and 1024 in the
+// backward (four rows per workgroup, sums on DPP with no LDS), beyond that to
+// 256, 512 or 1024 threads with one LDS exchange per sum.  Columns go in
+// pieces of eight per lane; rows of a width that is no multiple of eight start
+// at any element, so the 16-byte accesses are declared with element alignment
+// (the hardware takes them at any address) and the row's last few columns go
+// one by one.
 #include "gdn_device.h"
 #include "gdn_launch.h"
 #include "gdn_row.h"
@@ -100,7 +101,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const XT *x
 // as its loads, its sum and its stores one after the other, so the next row's
 // loads are issued before this row's sum (AHEAD; not at 1024 threads, whose
 // registers do not hold two rows): 32768 x 1024 in bf16 43.1 -> 39.6 us, 5.1
-// TB/s.  Beyond 8192 columns a few registers spill; the loads still bound it.
+// TB/s.  Up to 8192 columns nothing spills and the loads bound it (4.8 to 5.3
+// TB/s of dy, r and dx from 32 million elements on).  Beyond, registers spill
+// to scratch memory with an fp32 r (80 and 140 bytes a thread), beyond 16384
+// columns with any (128 to 232), and the rate falls: 4096 x 16384 86 us in bf16
+// (4.7 TB/s), 180 with an fp32 r, 237 in fp32 (3.4); 4096 x 32768 247, 380
+// and 409 us (3.3, 3.5 and 3.9 TB/s).
 template <class DT, class RT, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(const DT *dy, const RT *r, const float *w,
                                                                          const float *rstd, const RT *dr, RT *dx,

@@ -388,7 +388,7 @@ gdn_status gdn_gated_rmsnorm(const float *o, const void *z, const float *weight,
  *   y_scale  [rows] fp32: required with 8-bit output, null otherwise
  * 1 <= D <= 32768, any value.  x, residual, y and r are 16-byte aligned
  * (8-bit y: 8-byte); rows need not be.  A row that holds an infinity or a NaN
- * gives NaN codes and scale in 8 bits.  u^2 must not overflow fp32.
+ * gives NaN codes and scale in 8 bits.  The sum of u^2 must not overflow fp32.
  * Errors: GDN_ERR_INVALID_ARG (null required pointers, a y_scale or r that
  * does not belong, rows < 1, D < 1, eps <= 0, misalignment, an output that
  * overlaps an input or another output), GDN_ERR_UNSUPPORTED (D > 32768 or
@@ -421,7 +421,8 @@ gdn_status gdn_add_rmsnorm_bwd(const void *dy, const void *r, const float *weigh
 /*
  * gdn_quantize_rows -- rows in 8 bits with one scale each, for the weights
  * and activations of gdn_linear that no norm quantises:
- *   scale = max|x| / 448 (1 for a row of zeros);  q = e4m3(x / scale)
+ *   scale = max|x| / 448 (1 where that is zero in fp32: a row of zeros, or of
+ *   numbers below 3e-43);  q = e4m3(x / scale)
  *   x [rows, D] dtype (GDN_BF16 or GDN_F32), 16-byte aligned;
  *   q [rows, D] e4m3, 8-byte aligned;  scale [rows] fp32
  * A row that holds a NaN has NaN as its scale and codes; one with an infinity
