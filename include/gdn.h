@@ -435,7 +435,7 @@ gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long row
 /* Activation of gdn_linear: none, max(z, 0), z sigmoid(z), z Phi(z) with the
  * normal distribution function Phi.  In fp32 arithmetic: sigmoid is within
  * 2^-22 |z| + 2^-20 of itself, Phi within 2^-20 of itself (2^-16 for bf16
- * outputs, below -6) down to z = -13, where it leaves fp32's normal range. */
+ * outputs) down to z = -13, where it leaves fp32's normal range. */
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_RELU = 1, GDN_ACT_SILU = 2, GDN_ACT_GELU = 3 } gdn_act;
 
 /*
