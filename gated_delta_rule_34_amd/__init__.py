@@ -21,6 +21,8 @@ __all__ = [
     "gdn_add_rmsnorm", "gdn_add_rmsnorm_bwd", "gdn_add_rmsnorm_bwd_workspace", "gdn_quantize_rows",
     "gdn_linear", "gdn_linear_workspace", "gdn_linear_bwd", "gdn_linear_bwd_workspace",
     "gdn_linear_plan", "gdn_linear_bwd_plan",
+    "gdn_add_layernorm", "gdn_add_layernorm_bwd", "gdn_add_layernorm_bwd_workspace",
+    "gdn_gated_linear", "gdn_gated_linear_workspace", "gdn_gated_linear_bwd", "gdn_gated_linear_bwd_workspace",
     "clock_probe",
     "GDN_F32", "GDN_BF16", "GDN_F8E4M3", "BT",
 ]
@@ -109,6 +111,20 @@ def load():
     lib.gdn_linear_bwd_plan.argtypes = [_i] * 9 + [_vp]
     lib.gdn_linear_bwd.restype = _i
     lib.gdn_linear_bwd.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
+    lib.gdn_add_layernorm.restype = _i
+    lib.gdn_add_layernorm.argtypes = [_vp] * 9 + [_ll, _i, _i, _i, _i, _f, _vp]
+    lib.gdn_add_layernorm_bwd_workspace.restype = _sz
+    lib.gdn_add_layernorm_bwd_workspace.argtypes = [_ll, _i]
+    lib.gdn_add_layernorm_bwd.restype = _i
+    lib.gdn_add_layernorm_bwd.argtypes = [_vp] * 9 + [_ll, _i, _i, _i, _vp, _sz, _vp]
+    lib.gdn_gated_linear_workspace.restype = _sz
+    lib.gdn_gated_linear_workspace.argtypes = [_i] * 4
+    lib.gdn_gated_linear.restype = _i
+    lib.gdn_gated_linear.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
+    lib.gdn_gated_linear_bwd_workspace.restype = _sz
+    lib.gdn_gated_linear_bwd_workspace.argtypes = [_i] * 9
+    lib.gdn_gated_linear_bwd.restype = _i
+    lib.gdn_gated_linear_bwd.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
     _lib = lib
     return lib
 
@@ -748,6 +764,84 @@ def gdn_add_rmsnorm_bwd(dy, r, weight, rstd, dr=None, need_dweight=True, workspa
     return dx, dw
 
 
+def gdn_add_layernorm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None, return_stats=False, out=None,
+                      residual_out=None):
+    """Residual addition and layer norm over the last axis: u = x + residual,
+    y = (u - mean(u)) / sqrt(var(u) + eps) * weight + bias.  bias [D] fp32 or None; the other arguments as
+    gdn_add_rmsnorm.  Returns (y, r, mean, rstd, y_scale): r = u in the type of residual (None without one), mean and
+    rstd [rows] when return_stats, y_scale [rows] for 8-bit y, None otherwise."""
+    torch = _torch()
+    shape, dev, f32 = tuple(x.shape), x.device, torch.float32
+    if not shape:
+        raise ValueError("x must have at least one axis")
+    D = shape[-1]
+    rows = x.numel() // D if D else 0
+    _need(x, "x", shape, x.dtype, dev)
+    _need(weight, "weight", (D,), f32, dev)
+    if bias is not None:
+        _need(bias, "bias", (D,), f32, dev)
+    rdt = x.dtype
+    r = None
+    if residual is not None:
+        rdt = residual.dtype
+        _need(residual, "residual", shape, rdt, dev)
+        r = residual_out if residual_out is not None else torch.empty_like(residual)
+        if r is residual_out:
+            _need(r, "residual_out", shape, rdt, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    odt = x.dtype if out_dtype is None else out_dtype
+    y = torch.empty_like(x, dtype=odt) if out is None else out
+    if out is not None:
+        _need(y, "out", shape, odt, dev)
+    mean = torch.empty(shape[:-1], dtype=f32, device=dev) if return_stats else None
+    rstd = torch.empty(shape[:-1], dtype=f32, device=dev) if return_stats else None
+    y_scale = torch.empty(shape[:-1], dtype=f32, device=dev) if odt == torch.float8_e4m3fn else None
+    _on_device(load().gdn_add_layernorm, "gdn_add_layernorm", dev,
+               _addr(x), _addr(residual), _addr(weight), _addr(bias), _addr(y), _addr(r), _addr(mean), _addr(rstd),
+               _addr(y_scale), rows, D, _code(x.dtype, "x"), _code(rdt, "residual"), _code(odt, "out_dtype"),
+               float(eps))
+    return y, r, mean, rstd, y_scale
+
+
+def gdn_add_layernorm_bwd_workspace(rows, D):
+    return int(load().gdn_add_layernorm_bwd_workspace(rows, D))
+
+
+def gdn_add_layernorm_bwd(dy, r, weight, mean, rstd, dr=None, need_dweight=True, need_dbias=True, workspace=None):
+    """Gradients of gdn_add_layernorm.  dy [..., D] bf16 or fp32; r [..., D]: what the forward returned (x when it had
+    no residual); mean, rstd [...] fp32; dr [..., D]: gradient that reaches r from elsewhere, or None.  Returns (dx in
+    the type of r: the gradient of x and of residual alike, dweight, dbias [D] fp32 or None)."""
+    torch = _torch()
+    shape, dev, f32 = tuple(dy.shape), dy.device, torch.float32
+    if not shape:
+        raise ValueError("dy must have at least one axis")
+    D = shape[-1]
+    rows = dy.numel() // D if D else 0
+    _need(dy, "dy", shape, dy.dtype, dev)
+    _need(r, "r", shape, r.dtype, dev)
+    _need(weight, "weight", (D,), f32, dev)
+    _need(mean, "mean", shape[:-1], f32, dev)
+    _need(rstd, "rstd", shape[:-1], f32, dev)
+    if dr is not None:
+        _need(dr, "dr", shape, r.dtype, dev)
+    dx = torch.empty_like(r)
+    dw = torch.empty((D,), dtype=f32, device=dev) if need_dweight else None
+    db = torch.empty((D,), dtype=f32, device=dev) if need_dbias else None
+    ws, nbytes = None, 0
+    lib = load()
+    if need_dweight or need_dbias:
+        if workspace is None:
+            nbytes = lib.gdn_add_layernorm_bwd_workspace(rows, D)
+            ws = _scratch(nbytes, dev)
+        else:
+            ws, nbytes = workspace, _given(workspace, dev)
+    _on_device(lib.gdn_add_layernorm_bwd, "gdn_add_layernorm_bwd", dev,
+               _addr(dy), _addr(r), _addr(weight), _addr(mean), _addr(rstd), _addr(dr), _addr(dx), _addr(dw), _addr(db),
+               rows, D, _code(dy.dtype, "dy"), _code(r.dtype, "r"), _addr(ws), nbytes)
+    return dx, dw, db
+
+
 def gdn_quantize_rows(x):
     """Rows of x [..., D] (bf16 or fp32) in 8 bits: (q float8_e4m3fn [..., D], scale [...] fp32) with
     scale = max|x| / 448 (1 for a row of zeros) and q = x / scale."""
@@ -895,6 +989,102 @@ def gdn_linear_bwd_plan(M, N, K, dy_code, grad_code, act, need_dx=True, need_dw=
     _check(load().gdn_linear_bwd_plan(M, N, K, dy_code, grad_code, _act_code(act), int(need_dx), int(need_dw),
                                       int(need_dbias), plan), "gdn_linear_bwd_plan")
     return {"parts": plan[0], "pair": plan[1], "dx": dict(zip(_CUT, plan[2:6])), "dw": dict(zip(_CUT, plan[6:10]))}
+
+
+def gdn_gated_linear_workspace(M, N, K, dtype_code):
+    return int(load().gdn_gated_linear_workspace(M, N, K, dtype_code))
+
+
+def _halves(weight):
+    if weight.dim() != 2 or weight.shape[0] % 2:
+        raise ValueError(f"weight must be [2 N, K], got {tuple(weight.shape)}")
+    return weight.shape[0] // 2
+
+
+def gdn_gated_linear(x, weight, bias=None, act="silu", x_scale=None, w_scale=None, out_dtype=None,
+                     return_preact=False, workspace=None, out=None):
+    """Gated projection in one kernel: (g, u) = (x weight^T) x_scale w_scale + bias, y = act(g) u.  x [..., K], weight
+    [2 N, K] (N gate rows, then N up rows), both bf16, or both float8_e4m3fn with x_scale [...] and w_scale [2 N] fp32;
+    bias [2 N] fp32; act: none, relu, silu or gelu.  K is a multiple of 8 (16 in 8 bits).  Returns (y [..., N] in
+    out_dtype: bf16, the default, or fp32; z [..., 2 N] bf16 or None): z, that is g and u, with return_preact."""
+    torch = _torch()
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    N, K = _halves(weight), x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    _need(x, "x", lead + (K,), dt, dev)
+    _need(weight, "weight", (2 * N, K), dt, dev)
+    M = x.numel() // K if K else 0
+    if dt == torch.float8_e4m3fn:
+        _need(x_scale, "x_scale", lead, f32, dev)
+        _need(w_scale, "w_scale", (2 * N,), f32, dev)
+    elif x_scale is not None or w_scale is not None:
+        raise ValueError("x_scale and w_scale belong to float8_e4m3fn operands")
+    if bias is not None:
+        _need(bias, "bias", (2 * N,), f32, dev)
+    _multiple(K, 16 if dt == torch.float8_e4m3fn else 8)
+    odt = torch.bfloat16 if out_dtype is None else out_dtype
+    y = torch.empty(lead + (N,), dtype=odt, device=dev) if out is None else out
+    if out is not None:
+        _need(y, "out", lead + (N,), odt, dev)
+    z = torch.empty(lead + (2 * N,), dtype=torch.bfloat16, device=dev) if return_preact else None
+    lib = load()
+    code, ocode = _code(dt, "x"), _code(odt, "out_dtype")
+    ws = workspace
+    if ws is None:
+        nbytes = lib.gdn_gated_linear_workspace(M, N, K, code)
+        if nbytes:
+            ws = _scratch(nbytes, dev)
+    else:
+        nbytes = _given(ws, dev)
+    _on_device(lib.gdn_gated_linear, "gdn_gated_linear", dev,
+               _addr(x), _addr(weight), _addr(x_scale), _addr(w_scale), _addr(bias), _addr(y), _addr(z), M, N, K, code,
+               ocode, _act_code(act), _addr(ws), nbytes)
+    return y, z
+
+
+def gdn_gated_linear_bwd_workspace(M, N, K, dy_code, grad_code, act, need_dx=True, need_dw=True, need_dbias=False):
+    return int(load().gdn_gated_linear_bwd_workspace(M, N, K, dy_code, grad_code, _act_code(act), int(need_dx),
+                                                     int(need_dw), int(need_dbias)))
+
+
+def gdn_gated_linear_bwd(dy, x, weight, z, act="silu", bias=False, grad_dtype=None, need_dx=True, need_dw=True,
+                         workspace=None):
+    """Gradients of gdn_gated_linear with bf16 x [..., K] and weight [2 N, K]: dg = dy u act'(g), du = dy act(g),
+    dx = (dg, du) weight, dw = (dg, du)^T x, dbias = (dg, du) summed over rows.  dy [..., N] bf16 or fp32; z [..., 2 N]
+    bf16: what the forward returned with return_preact.  grad_dtype of dx and dw: bf16 (default; dg and du are rounded
+    to bf16 for the products) or fp32 (they are not rounded).  Returns (dx, dw [2 N, K], dbias [2 N] fp32), None for
+    what is not asked for."""
+    torch = _torch()
+    dev, bf = dy.device, torch.bfloat16
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    N, K = _halves(weight), x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    _need(x, "x", lead + (K,), bf, dev)
+    _need(weight, "weight", (2 * N, K), bf, dev)
+    _need(dy, "dy", lead + (N,), dy.dtype, dev)
+    _need(z, "z", lead + (2 * N,), bf, dev)
+    _multiple(K, 8)
+    M = x.numel() // K if K else 0
+    gdt = bf if grad_dtype is None else grad_dtype
+    dx = torch.empty_like(x, dtype=gdt) if need_dx else None
+    dw = torch.empty_like(weight, dtype=gdt) if need_dw else None
+    db = torch.empty((2 * N,), dtype=torch.float32, device=dev) if bias else None
+    lib = load()
+    a, dyc, gc = _act_code(act), _code(dy.dtype, "dy"), _code(gdt, "grad_dtype")
+    ws = workspace
+    if ws is None:
+        nbytes = lib.gdn_gated_linear_bwd_workspace(M, N, K, dyc, gc, a, int(need_dx), int(need_dw), int(bool(bias)))
+        if nbytes:
+            ws = _scratch(nbytes, dev)
+    else:
+        nbytes = _given(ws, dev)
+    _on_device(lib.gdn_gated_linear_bwd, "gdn_gated_linear_bwd", dev,
+               _addr(dy), _addr(x), _addr(weight), _addr(z), _addr(dx), _addr(dw), _addr(db), M, N, K, dyc, gc, a,
+               _addr(ws), nbytes)
+    return dx, dw, db
 
 
 def clock_probe(nblocks=256, spin_us=2000, device="cuda"):

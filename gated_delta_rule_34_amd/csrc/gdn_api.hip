@@ -679,6 +679,55 @@ gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long row
     return from_hip(gdn::launch_quantize_rows(x, q, scale, (long)rows, D, dtype == GDN_BF16, (hipStream_t)stream));
 }
 
+gdn_status gdn_add_layernorm(const void *x, const void *residual, const float *weight, const float *bias, void *y,
+                             void *r, float *mean, float *rstd, float *y_scale, long long rows, int D,
+                             gdn_dtype dtype, gdn_dtype rdtype, gdn_dtype out_dtype, float eps, void *stream) {
+    if (!x || !weight || !y || !rows_ok(rows, D) || !(eps > 0.f)) return GDN_ERR_INVALID_ARG;
+    if (!norm_types_ok(dtype, rdtype) || D > gdn::kMaxNormCols) return GDN_ERR_UNSUPPORTED;
+    const bool f8 = out_dtype == GDN_F8E4M3;
+    if (!f8 && out_dtype != dtype) return GDN_ERR_UNSUPPORTED;
+    if (f8 != (y_scale != nullptr) || (r && !residual)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(r, 16) || !aligned(y, f8 ? 8 : 16) || !aligned(weight, 4) ||
+        !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(y_scale, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t n = (size_t)rows * D;
+    const Range ins[] = {{x, n * esize3(dtype)}, {weight, (size_t)D * 4}, {bias, (size_t)D * 4},
+                         {r == residual ? nullptr : residual, n * esize3(rdtype)}};
+    const Range outs[] = {{y, n * esize3(out_dtype)}, {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4},
+                          {y_scale, (size_t)rows * 4}, {r, n * esize3(rdtype)}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_add_layernorm(x, residual, weight, bias, y, r, mean, rstd, y_scale, (long)rows, D,
+                                              dtype == GDN_BF16, rdtype == GDN_BF16, f8, eps, (hipStream_t)stream));
+}
+
+size_t gdn_add_layernorm_bwd_workspace(long long rows, int D) {
+    if (!rows_ok(rows, D) || D > gdn::kMaxNormCols) return 0;
+    return align_up((size_t)gdn::ln_bwd_blocks((long)rows, D) * 2 * D * sizeof(float));
+}
+
+gdn_status gdn_add_layernorm_bwd(const void *dy, const void *r, const float *weight, const float *mean,
+                                 const float *rstd, const void *dr, void *dx, float *dweight, float *dbias,
+                                 long long rows, int D, gdn_dtype dtype, gdn_dtype rdtype, void *ws, size_t ws_bytes,
+                                 void *stream) {
+    if (!dy || !r || !weight || !mean || !rstd || !dx || !rows_ok(rows, D)) return GDN_ERR_INVALID_ARG;
+    if (!norm_types_ok(dtype, rdtype) || D > gdn::kMaxNormCols) return GDN_ERR_UNSUPPORTED;
+    if (!aligned(dy, 16) || !aligned(r, 16) || !aligned(dr, 16) || !aligned(dx, 16) || !aligned(weight, 4) ||
+        !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+        return GDN_ERR_INVALID_ARG;
+    const bool sums = dweight || dbias;
+    const size_t need = sums ? gdn_add_layernorm_bwd_workspace(rows, D) : 0;
+    if (sums && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    const size_t n = (size_t)rows * D;
+    const Range ins[] = {{dy, n * esize3(dtype)}, {r, n * esize3(rdtype)}, {weight, (size_t)D * 4},
+                         {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4}, {dr, n * esize3(rdtype)}};
+    const Range outs[] = {{dx, n * esize3(rdtype)}, {dweight, (size_t)D * 4}, {dbias, (size_t)D * 4},
+                          {sums ? ws : nullptr, need}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_add_layernorm_bwd(dy, r, weight, mean, rstd, dr, dx, dweight, dbias, (float *)ws,
+                                                  (long)rows, D, dtype == GDN_BF16, rdtype == GDN_BF16,
+                                                  (hipStream_t)stream));
+}
+
 // Sizes of a product the kernels index: 32-bit offsets within a tile of 256
 // rows (N, K), a grid of fewer than 2^32 threads (the tiles of each output:
 // M x N in the forward, M x K and N x K in the backward, which reads M x N).
@@ -757,6 +806,71 @@ gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const vo
     if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
     return from_hip(gdn::launch_linear_bwd(plan, dy, x, w, z, dx, dw, dbias, M, N, K, dy_dtype == GDN_F32,
                                            grad_dtype == GDN_F32, (int)act, (char *)ws, (hipStream_t)stream));
+}
+
+// A gated product is one of 2 N columns.
+static gdn_status gated_check(int M, int N, int K, gdn_dtype dtype, bool bwd) {
+    if (N < 1) return GDN_ERR_INVALID_ARG;
+    return linear_check(M, N > (1 << 21) ? (1 << 22) + 1 : 2 * N, K, dtype, bwd);  // too many columns either way
+}
+
+size_t gdn_gated_linear_workspace(int M, int N, int K, gdn_dtype dtype) {
+    if (gated_check(M, N, K, dtype, false) != GDN_OK) return 0;
+    return align_up(gdn::linear_ws_bytes(gdn::linear_plan(M, 2 * N, K, dtype == GDN_F8E4M3), M, 2 * N));
+}
+
+gdn_status gdn_gated_linear(const void *x, const void *w, const float *x_scale, const float *w_scale,
+                            const float *bias, void *y, void *z, int M, int N, int K, gdn_dtype dtype,
+                            gdn_dtype out_dtype, gdn_act act, void *ws, size_t ws_bytes, void *stream) {
+    if (!x || !w || !y) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = gated_check(M, N, K, dtype, false);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(out_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
+    const bool f8 = dtype == GDN_F8E4M3;
+    if (f8 != (x_scale != nullptr) || f8 != (w_scale != nullptr)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(z, 16) || !aligned(x_scale, 4) ||
+        !aligned(w_scale, 4) || !aligned(bias, 4))
+        return GDN_ERR_INVALID_ARG;
+    const gdn::MmPlan plan = gdn::linear_plan(M, 2 * N, K, f8);
+    const size_t need = align_up(gdn::linear_ws_bytes(plan, M, 2 * N));
+    if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    const size_t mn = (size_t)M * N;
+    const Range ins[] = {{x, (size_t)M * K * esize3(dtype)}, {w, (size_t)2 * N * K * esize3(dtype)},
+                         {x_scale, (size_t)M * 4}, {w_scale, (size_t)N * 8}, {bias, (size_t)N * 8}};
+    const Range outs[] = {{y, mn * esize3(out_dtype)}, {z, mn * 4}, {need ? ws : nullptr, need}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_gated_linear(plan, x, w, x_scale, w_scale, bias, y, z, M, N, K, f8, out_dtype == GDN_F32,
+                                             (int)act, (float *)ws, (hipStream_t)stream));
+}
+
+size_t gdn_gated_linear_bwd_workspace(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
+                                      int need_dx, int need_dw, int need_dbias) {
+    if (gated_check(M, N, K, GDN_BF16, true) != GDN_OK || !dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act))
+        return 0;
+    return gdn::gated_linear_bwd_plan(M, N, K, grad_dtype == GDN_F32, need_dx != 0, need_dw != 0, need_dbias != 0).total;
+}
+
+gdn_status gdn_gated_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,
+                                float *dbias, int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype,
+                                gdn_act act, void *ws, size_t ws_bytes, void *stream) {
+    if (!dy || !x || !w || !z || (!dx && !dw && !dbias)) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = gated_check(M, N, K, GDN_BF16, true);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(dy_dtype) || !dtype_ok(grad_dtype) || !act_ok(act)) return GDN_ERR_UNSUPPORTED;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(z, 16) || !aligned(dx, 16) ||
+        !aligned(dw, 16) || !aligned(dbias, 4))
+        return GDN_ERR_INVALID_ARG;
+    const gdn::LinearBwdPlan plan = gdn::gated_linear_bwd_plan(M, N, K, grad_dtype == GDN_F32, dx != nullptr,
+                                                               dw != nullptr, dbias != nullptr);
+    const size_t need = plan.total;
+    if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return GDN_ERR_WORKSPACE;
+    const size_t mn = (size_t)M * N, mk = (size_t)M * K, nk = (size_t)2 * N * K;
+    const Range ins[] = {{dy, mn * esize3(dy_dtype)}, {x, mk * 2}, {w, nk * 2}, {z, mn * 4}};
+    const Range outs[] = {{dx, mk * esize3(grad_dtype)}, {dw, nk * esize3(grad_dtype)}, {dbias, (size_t)N * 8},
+                          {ws, need}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_gated_linear_bwd(plan, dy, x, w, z, dx, dw, dbias, M, N, K, dy_dtype == GDN_F32,
+                                                 grad_dtype == GDN_F32, (int)act, (char *)ws, (hipStream_t)stream));
 }
 
 static void plan_ints(const gdn::MmPlan &p, int *out) {

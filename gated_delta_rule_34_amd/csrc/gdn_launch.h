@@ -178,5 +178,34 @@ LinearBwdPlan linear_bwd_plan(int M, int N, int K, bool dy_f32, bool grad_f32, i
 hipError_t launch_linear_bwd(const LinearBwdPlan &p, const void *dy, const void *x, const void *w, const void *z,
                              void *dx, void *dw, float *dbias, int M, int N, int K, bool dy_f32, bool grad_f32, int act,
                              char *ws, hipStream_t st);
+// The second half of it, from the planes of dz (p.Np columns each) and, with
+// dbias, the p.blocks rows of its partial sums in ws: a row for every
+// dz_rows(M, N) rows of dz.
+int dz_rows(int M, int N);
+hipError_t launch_linear_grads(const LinearBwdPlan &p, const void *dz, const void *x, const void *w, void *dx, void *dw,
+                               float *dbias, int M, int N, int K, bool grad_f32, char *ws, hipStream_t st);
+
+// The gated projection (gdn_gated.hip): w [2 N, K], N gate rows, then N up
+// rows; y = act(gate) up [M, N], z [M, 2 N] the arguments.  Cut like a product
+// of 2 N columns.
+hipError_t launch_gated_linear(const MmPlan &p, const void *x, const void *w, const float *xs, const float *ws,
+                               const float *bias, void *y, void *z, int M, int N, int K, bool f8, bool y_f32, int act,
+                               float *part, hipStream_t st);
+// Its backward.
+LinearBwdPlan gated_linear_bwd_plan(int M, int N, int K, bool grad_f32, bool dx, bool dw, bool dbias);
+hipError_t launch_gated_linear_bwd(const LinearBwdPlan &p, const void *dy, const void *x, const void *w, const void *z,
+                                   void *dx, void *dw, float *dbias, int M, int N, int K, bool dy_f32, bool grad_f32,
+                                   int act, char *ws, hipStream_t st);
+
+// Residual layer norm (gdn_layernorm.hip); arguments as the RMS norm's, b and
+// mean nullable.  Backward: part holds ln_bwd_blocks(rows, D) rows of 2 D
+// partial column sums (used when dw or db is wanted).
+hipError_t launch_add_layernorm(const void *x, const void *res, const float *w, const float *b, void *y, void *rout,
+                                float *mean, float *rstd, float *yscale, long rows, int D, bool x_bf16, bool r_bf16,
+                                bool f8, float eps, hipStream_t st);
+int ln_bwd_blocks(long rows, int D);
+hipError_t launch_add_layernorm_bwd(const void *dy, const void *r, const float *w, const float *mean,
+                                    const float *rstd, const void *dr, void *dx, float *dw, float *db, float *part,
+                                    long rows, int D, bool dy_bf16, bool r_bf16, hipStream_t st);
 
 }  // namespace gdn

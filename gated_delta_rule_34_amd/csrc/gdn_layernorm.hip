@@ -1,0 +1,348 @@
+// gdn_layernorm.hip -- residual addition and layer norm in one pass (with an
+// output in the input's type or in e4m3 with one scale per row), and its
+// backward.
+//   forward   u = x + residual;  r = u in the residual's type
+//             m = mean(u), s = (mean((u - m)^2) + eps)^-1/2;  y = (u - m) s w + b
+//   8 bits    scale = max|y| / 448,  q = e4m3(y / scale)
+//   backward  xhat = (r - m) s,  a = w dy
+//             dx = s (a - mean(a) - xhat mean(a xhat)) + dr
+//             dw = sum over rows of dy xhat,  db = sum over rows of dy
+// Everything is fp32 between the loads and one rounding at the stores.  The
+// variance is taken of the differences to the mean, in a second turn over the
+// registers that hold the row: the difference of the two moments would lose
+// all bits where the mean is large beside the spread.  Bound by HBM: a row is
+// read once, held in registers while its sums are formed, and written once.
+// Rows are laid over threads as in the RMS norm: one wave up to 2048 columns
+// in the forward and 1024 in the backward, beyond that 256, 512 or 1024
+// threads with one LDS exchange per sum; columns in pieces of eight per
+// thread at element alignment.
+#include "gdn_device.h"
+#include "gdn_launch.h"
+#include "gdn_row.h"
+#include "gdn_tile.h"
+
+namespace gdn {
+
+template <class XT, class RT, class OT, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, const RT *res, const float *w,
+                                                                   const float *b, OT *y, RT *rout, float *mean,
+                                                                   float *rstd, float *yscale, long rows, int D,
+                                                                   float eps) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
+    constexpr bool F8 = sizeof(OT) == 1;
+    __shared__ float sh[3][TPR / 64 + 1];
+    const int tid = threadIdx.x % TPR;
+    const long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (row >= rows) return;  // whole waves leave, and only where a row is one wave
+    const XT *xr = x + row * D;
+    float u[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load_piece(u[i], xr, (tid + i * TPR) * 8, D);
+    if (res) {
+        const RT *rr = res + row * D;
+        float t[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load_piece(t[i], rr, (tid + i * TPR) * 8, D);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[i][e] += t[i][e];
+        if (rout)  // may be res itself: this thread has read what it replaces
+#pragma unroll
+            for (int i = 0; i < NV; ++i) store_piece(rout + row * D, u[i], (tid + i * TPR) * 8, D);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += u[i][e];
+    const float m = row_sum<TPR>(sum, sh[0]) / (float)D;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int left = D - (tid + i * TPR) * 8;  // columns of this piece and after it
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            u[i][e] = e < left ? u[i][e] - m : 0.f;
+            ss = fmaf(u[i][e], u[i][e], ss);
+        }
+    }
+    ss = row_sum<TPR>(ss, sh[1]);
+    const float s = 1.f / sqrtf(ss / (float)D + eps);
+    if (tid == 0) {
+        if (mean) mean[row] = m;
+        if (rstd) rstd[row] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float wv[8], bv[8];
+        load_piece(wv, w, (tid + i * TPR) * 8, D);
+        if (b) load_piece(bv, b, (tid + i * TPR) * 8, D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            u[i][e] *= s;
+            u[i][e] = b ? fmaf(u[i][e], wv[e], bv[e]) : u[i][e] * wv[e];
+        }
+    }
+    if constexpr (F8) {
+        // largest magnitude, compared as bits: an infinity or NaN in the row
+        // wins, so such a row's scale and codes show it
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(u[i][e]) & 0x7fffffffu);
+        am = row_max<TPR>(am, (uint32_t *)sh[2]);
+        float scale = __uint_as_float(am) * (1.f / 448.f);
+        if (scale == 0.f) scale = 1.f;
+        if (tid == 0) yscale[row] = scale;
+        const QuantRow q(scale);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) store_piece_f8((uint8_t *)y + row * D, u[i], q, (tid + i * TPR) * 8, D);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) store_piece(y + row * D, u[i], (tid + i * TPR) * 8, D);
+    }
+}
+
+// Two sums over the TPR threads of a row in one exchange; sh holds TPR / 64
+// pairs and is written once per call.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2 *sh) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) {
+            a += sh[i].x;
+            b += sh[i].y;
+        }
+    }
+    return make_float2(a, b);
+}
+
+// Backward.  A workgroup walks rows (its first row, then every RPB * grid rows
+// on) and keeps the column sums of dy xhat and dy in registers; they leave as
+// one row of 2 D partial sums per workgroup, which ln_colsum_kernel adds up in
+// a fixed order (no atomics, so results repeat bit for bit).  The next row's
+// loads are issued before this row's sums where the registers hold both
+// (AHEAD).
+template <class DT, class RT, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT *dy, const RT *r, const float *w,
+                                                                       const float *mean, const float *rstd,
+                                                                       const RT *dr, RT *dx, float *part, long rows,
+                                                                       int D) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr bool AHEAD = TPR < 1024 && !(NV == 4 && sizeof(RT) == 4);
+    using DRaw = typename RawOf<DT>::type;
+    using RRaw = typename RawOf<RT>::type;
+    __shared__ float2 sh[2][TPR / 64 + 1];
+    __shared__ float shw[RPB > 1 ? RPB * TPR * 8 : 1];
+    const int tid = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    f32x8 aw[NV], ab[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) aw[i] = ab[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    DRaw g0[NV];
+    RRaw r0[NV], d0[NV];
+    float m0 = 0.f, s0 = 0.f;
+    auto load = [&](long row) {
+        m0 = mean[row];
+        s0 = rstd[row];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) g0[i] = load_raw(dy + row * D, (tid + i * TPR) * 8, D);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) r0[i] = load_raw(r + row * D, (tid + i * TPR) * 8, D);
+        if (dr) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) d0[i] = load_raw(dr + row * D, (tid + i * TPR) * 8, D);
+        }
+    };
+    const long step = (long)gridDim.x * RPB;
+    long row = (long)blockIdx.x * RPB + grp;
+    if (AHEAD && row < rows) load(row);
+    for (int turn = 0; row < rows; row += step, turn ^= 1) {
+        if (!AHEAD) load(row);
+        f32x8 g[NV], xh[NV];
+        RRaw d1[NV];
+        const float s = s0, m = m0;
+        float dot = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            // past the row's end dy and w are zero, so what xhat holds there does not count
+            const f32x8 wv = load8v(w, (tid + i * TPR) * 8, D);
+            g[i] = raw_f32(g0[i]);
+            xh[i] = raw_f32(r0[i]);
+            d1[i] = d0[i];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[i][e] = (xh[i][e] - m) * s;
+                aw[i][e] = fmaf(g[i][e], xh[i][e], aw[i][e]);
+                ab[i][e] += g[i][e];
+                g[i][e] *= wv[e];
+                sum += g[i][e];
+                dot = fmaf(g[i][e], xh[i][e], dot);
+            }
+        }
+        if (AHEAD && row + step < rows) load(row + step);
+        // the two halves of sh alternate, so a fast wave of the next row does
+        // not overwrite sums that a slow one still reads
+        const float2 both = row_sum2<TPR>(dot, sum, sh[turn]);
+        dot = both.x / (float)D;
+        sum = both.y / (float)D;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            f32x8 v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = s * (g[i][e] - sum - xh[i][e] * dot);
+            if (dr) {
+                const f32x8 d = raw_f32(d1[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += d[e];
+            }
+            store8v(dx + row * D, v, (tid + i * TPR) * 8, D);
+        }
+    }
+    if (!part) return;
+    float *pr = part + (long)blockIdx.x * 2 * D;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x8(&acc)[NV] = h ? ab : aw;
+        if constexpr (RPB > 1) {  // add the workgroup's rows of sums, in order
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) shw[(grp * 8 + e) * TPR + tid] = acc[i][e];
+                __syncthreads();
+                if (grp == 0) {
+                    f32x8 v;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = 0.f;
+#pragma unroll
+                        for (int p = 0; p < RPB; ++p) v[e] += shw[(p * 8 + e) * TPR + tid];
+                    }
+                    store8v(pr + h * D, v, (tid + i * TPR) * 8, D);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) store8v(pr + h * D, acc[i], (tid + i * TPR) * 8, D);
+        }
+    }
+}
+
+// dw[c], db[c] (nullable) = sums over n rows of part [n, 2 D]: 32 columns and
+// 32 row strides per workgroup, so that the loads of a column are in flight
+// together.
+__global__ __launch_bounds__(1024) void ln_colsum_kernel(const float *part, float *dw, float *db, int n, int D) {
+    __shared__ float sh[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int groups = (D + 31) / 32, h = blockIdx.x >= (unsigned)groups;
+    float *out = h ? db : dw;
+    if (!out) return;
+    const int c = ((int)blockIdx.x - h * groups) * 32 + tx;
+    float v = 0.f;
+    if (c < D) {
+        const float *p = part + h * D + c;
+#pragma unroll 8
+        for (int i = ty; i < n; i += 32) v += p[(long)i * 2 * D];
+    }
+    sh[ty][tx] = v;
+    __syncthreads();
+    if (ty == 0 && c < D) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += sh[i][tx];
+        out[c] = s;
+    }
+}
+
+template <class XT, class RT, class OT>
+static hipError_t launch_ln_t(const void *x, const void *res, const float *w, const float *b, void *y, void *rout,
+                              float *mean, float *rstd, float *yscale, long rows, int D, float eps, hipStream_t st) {
+    // a launch holds fewer than 2^32 threads: more rows than 2^21 workgroups
+    // take go in several launches
+#define GDN_LN(TPRv, NVv)                                                                                       \
+    if (D <= TPRv * NVv * 8) {                                                                                  \
+        constexpr int rpb = TPRv < 256 ? 256 / TPRv : 1;                                                        \
+        constexpr long most = (long)rpb << 21;                                                                  \
+        for (long r0 = 0; r0 < rows; r0 += most) {                                                              \
+            const long n = rows - r0 < most ? rows - r0 : most;                                                 \
+            hipLaunchKernelGGL((ln_kernel<XT, RT, OT, TPRv, NVv>), dim3((unsigned)((n + rpb - 1) / rpb)),       \
+                               dim3(TPRv < 256 ? 256 : TPRv), 0, st, (const XT *)x + r0 * D,                    \
+                               res ? (const RT *)res + r0 * D : nullptr, w, b, (OT *)y + r0 * D,                \
+                               rout ? (RT *)rout + r0 * D : nullptr, mean ? mean + r0 : nullptr,                \
+                               rstd ? rstd + r0 : nullptr, yscale ? yscale + r0 : nullptr, n, D, eps);          \
+            const hipError_t e = hipGetLastError();                                                             \
+            if (e != hipSuccess) return e;                                                                      \
+        }                                                                                                       \
+        return hipSuccess;                                                                                      \
+    }
+    GDN_LN(64, 1)
+    GDN_LN(64, 2)
+    GDN_LN(64, 4)
+    GDN_LN(256, 2)
+    GDN_LN(256, 4)
+    GDN_LN(512, 4)
+    GDN_LN(1024, 4)
+#undef GDN_LN
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_add_layernorm(const void *x, const void *res, const float *w, const float *b, void *y, void *rout,
+                                float *mean, float *rstd, float *yscale, long rows, int D, bool x_bf16, bool r_bf16,
+                                bool f8, float eps, hipStream_t st) {
+#define GDN_LN_T(XT, RT, OT) launch_ln_t<XT, RT, OT>(x, res, w, b, y, rout, mean, rstd, yscale, rows, D, eps, st)
+    if (x_bf16 && r_bf16) return f8 ? GDN_LN_T(uint16_t, uint16_t, uint8_t) : GDN_LN_T(uint16_t, uint16_t, uint16_t);
+    if (x_bf16) return f8 ? GDN_LN_T(uint16_t, float, uint8_t) : GDN_LN_T(uint16_t, float, uint16_t);
+    if (!r_bf16) return f8 ? GDN_LN_T(float, float, uint8_t) : GDN_LN_T(float, float, float);
+#undef GDN_LN_T
+    return hipErrorInvalidValue;
+}
+
+// Workgroups of the backward, as measured for the RMS norm's.
+int ln_bwd_blocks(long rows, int D) { return norm_bwd_blocks(rows, D); }
+
+template <class DT, class RT>
+static hipError_t launch_ln_bwd_t(const void *dy, const void *r, const float *w, const float *mean, const float *rstd,
+                                  const void *dr, void *dx, float *dw, float *db, float *part, long rows, int D,
+                                  hipStream_t st) {
+    const int nb = ln_bwd_blocks(rows, D);
+    float *pp = dw || db ? part : nullptr;
+#define GDN_LNB(MOST, TPRv, NVv)                                                                                      \
+    if (D <= MOST) {                                                                                                  \
+        hipLaunchKernelGGL((ln_bwd_kernel<DT, RT, TPRv, NVv>), dim3((unsigned)nb), dim3(TPRv < 256 ? 256 : TPRv), 0, \
+                           st, (const DT *)dy, (const RT *)r, w, mean, rstd, (const RT *)dr, (RT *)dx, pp, rows, D);  \
+    } else
+    GDN_LNB(512, 64, 1)
+    GDN_LNB(1024, 64, 2)
+    GDN_LNB(2048, 256, 1)
+    GDN_LNB(4096, 256, 2)
+    GDN_LNB(6144, 256, 3)
+    GDN_LNB(8192, 512, 2)
+    GDN_LNB(16384, 512, 4)
+    GDN_LNB(kMaxNormCols, 1024, 4) return hipErrorInvalidValue;
+#undef GDN_LNB
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || !pp) return err;
+    const int groups = (D + 31) / 32;
+    hipLaunchKernelGGL(ln_colsum_kernel, dim3((unsigned)(db ? 2 * groups : groups)), dim3(1024), 0, st, part, dw, db,
+                       nb, D);
+    return hipGetLastError();
+}
+
+hipError_t launch_add_layernorm_bwd(const void *dy, const void *r, const float *w, const float *mean,
+                                    const float *rstd, const void *dr, void *dx, float *dw, float *db, float *part,
+                                    long rows, int D, bool dy_bf16, bool r_bf16, hipStream_t st) {
+    if (dy_bf16 && r_bf16)
+        return launch_ln_bwd_t<uint16_t, uint16_t>(dy, r, w, mean, rstd, dr, dx, dw, db, part, rows, D, st);
+    if (dy_bf16) return launch_ln_bwd_t<uint16_t, float>(dy, r, w, mean, rstd, dr, dx, dw, db, part, rows, D, st);
+    if (!r_bf16) return launch_ln_bwd_t<float, float>(dy, r, w, mean, rstd, dr, dx, dw, db, part, rows, D, st);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace gdn

@@ -44,6 +44,7 @@ struct MmArgs {
     int slabs;          // slabs of the whole sum: parts * ceil(K / slab)
     int per_split;      // slabs per split; splits = gridDim.y
     int ti, tj;         // tiles along i and j
+    long pair;          // gated products: bytes from a gate row of U to its up row
 };
 
 // Sixteen e4m3 values as two bf16 fragments (exact).
@@ -147,6 +148,20 @@ struct Stage {
         }
         wrap = part - (long)(per - 1) * step;
         rsrc = make_rsrc(p + plane * part + s * step, 0);
+    }
+    // The rows of a gated product: sixteen gate rows and the sixteen up rows
+    // `pair` bytes behind them in turn, so that the wave that holds a gate
+    // column's products holds those of its up column.  A wave's instructions
+    // are all of one kind.
+    __device__ __forceinline__ void init_pairs(const char *p, long ld, int row0, int rows, int Kb, long pair, int per, int s,
+                                               int lane, int wave) {
+        static_assert(!T && W % 4 == 0, "eight rows an instruction, four instructions a pair of sixteens");
+        init(p + (wave & 2 ? pair : 0), ld, row0, min(rows, R / 2), Kb, 0, per, 0, s, lane, wave);
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+            const int row = (wave + W * n) * 8 + (lane >> 3);
+            off[n] = (uint32_t)((row >> 5) * 16 + (row & 15)) * (uint32_t)ld + chunk[n];
+        }
     }
     // A slab past the end (live false) has no range: its loads write zeros and read nothing.
     __device__ __forceinline__ void bound(bool last, bool live) { rsrc[2] = (int)(live ? (last ? range_last : range) : 0u); }

@@ -432,6 +432,44 @@ gdn_status gdn_add_rmsnorm_bwd(const void *dy, const void *r, const float *weigh
 gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long rows, int D, gdn_dtype dtype,
                              void *stream);
 
+/*
+ * gdn_add_layernorm -- the block's entry with a layer norm in the place of the
+ * RMS norm.  Per row of D:
+ *   u = x + residual (u = x without one);  r = u
+ *   m = mean(u);  s = (mean((u - m)^2) + eps)^-1/2;  y = (u - m) s weight + bias
+ *   8-bit output: y_scale = max|.| / 448 of that (1 for a row of zeros),
+ *   y = e4m3(. / y_scale), rounded to nearest even
+ * All of it in fp32 with one rounding per output; m and s are taken of the fp32
+ * sum, before r is rounded to its type, s of the differences to m.
+ *   bias   [D] fp32, nullable
+ *   mean, rstd  [rows] fp32, nullable: m and s, for gdn_add_layernorm_bwd
+ *   the others as gdn_add_rmsnorm
+ * Sizes, types, alignment, special values and errors as gdn_add_rmsnorm.
+ */
+gdn_status gdn_add_layernorm(const void *x, const void *residual, const float *weight, const float *bias, void *y,
+                             void *r, float *mean, float *rstd, float *y_scale, long long rows, int D,
+                             gdn_dtype dtype, gdn_dtype rdtype, gdn_dtype out_dtype, float eps, void *stream);
+
+/*
+ * gdn_add_layernorm_bwd -- gradients of gdn_add_layernorm (not of the rounding
+ * to 8 bits) for L = sum(dy . y) + sum(dr . r):
+ *   xhat = (r - mean) rstd;  a = weight dy
+ *   dx = rstd (a - mean(a) - xhat mean(a xhat)) + dr
+ *   dweight = sum over rows of dy xhat;  dbias = sum over rows of dy
+ * dx is the gradient of x and of residual alike.
+ *   mean, rstd [rows] fp32;  dweight, dbias [D] fp32, nullable
+ *   ws  gdn_add_layernorm_bwd_workspace() bytes, 256-byte aligned (may be NULL
+ *       without dweight and dbias)
+ * The others, types, sizes, alignment and errors as gdn_add_rmsnorm_bwd.  The
+ * sums over rows are formed in a fixed order.
+ */
+size_t gdn_add_layernorm_bwd_workspace(long long rows, int D);
+
+gdn_status gdn_add_layernorm_bwd(const void *dy, const void *r, const float *weight, const float *mean,
+                                 const float *rstd, const void *dr, void *dx, float *dweight, float *dbias,
+                                 long long rows, int D, gdn_dtype dtype, gdn_dtype rdtype, void *ws, size_t ws_bytes,
+                                 void *stream);
+
 /* Activation of gdn_linear: none, max(z, 0), z sigmoid(z), z Phi(z) with the
  * normal distribution function Phi.  In fp32 arithmetic: sigmoid is within
  * 2^-22 |z| + 2^-20 of itself, Phi within 2^-20 of itself (2^-16 for bf16
@@ -521,6 +559,48 @@ gdn_status gdn_linear_bwd(const void *dy, const void *x, const void *w, const vo
 gdn_status gdn_linear_plan(int M, int N, int K, gdn_dtype dtype, int *plan);
 gdn_status gdn_linear_bwd_plan(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act, int need_dx,
                                int need_dw, int need_dbias, int *plan);
+
+/*
+ * gdn_gated_linear -- the gated feed-forward projection: both products, the
+ * activation and the multiplication in one kernel.
+ *   (g, u) = (x w^T) x_scale w_scale + bias;   y = act(g) u
+ *   x [M, K], w [2 N, K]: N gate rows, then N up rows.  Types and x_scale [M],
+ *            w_scale [2 N] as gdn_linear
+ *   bias     [2 N] fp32, nullable
+ *   y        [M, N] out_dtype: GDN_BF16 or GDN_F32
+ *   z        [M, 2 N] bf16, nullable: g, then u, for gdn_gated_linear_bwd
+ * y is computed from the unrounded g and u.  Arithmetic, parts of long sums,
+ * alignment, workspace and errors as gdn_linear; sizes as gdn_linear with 2 N
+ * in the place of N (gdn_linear_plan(M, 2 N, ..) is how a call is cut).
+ */
+size_t gdn_gated_linear_workspace(int M, int N, int K, gdn_dtype dtype);
+
+gdn_status gdn_gated_linear(const void *x, const void *w, const float *x_scale, const float *w_scale,
+                            const float *bias, void *y, void *z, int M, int N, int K, gdn_dtype dtype,
+                            gdn_dtype out_dtype, gdn_act act, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * gdn_gated_linear_bwd -- gradients of gdn_gated_linear with bf16 x and w, for
+ * L = sum(dy . y):
+ *   dg = dy u act'(g);  du = dy act(g);  dx = (dg, du) w;  dw = (dg, du)^T x
+ *   dbias = sum over rows of (dg, du)
+ * (GDN_ACT_RELU chooses: dg is zero where g <= 0, whatever dy and u hold there)
+ *   dy [M, N] dy_dtype (GDN_BF16 or GDN_F32);  z [M, 2 N] bf16, required
+ *   dx [M, K], dw [2 N, K]  grad_dtype (GDN_BF16 or GDN_F32), nullable
+ *   dbias [2 N] fp32, nullable
+ * (dg, du) takes part in the products as a bf16 operand: rounded once with
+ * GDN_BF16 gradients, as three bf16 parts that together carry its fp32 value
+ * with GDN_F32 ones (an infinity in w or x meets parts that are zero and gives
+ * NaN).  dbias sums the unrounded values in a fixed order.
+ * Alignment 16 bytes (dbias 4); workspace, sizes and errors as gdn_linear_bwd
+ * with 2 N in the place of N.
+ */
+size_t gdn_gated_linear_bwd_workspace(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype, gdn_act act,
+                                      int need_dx, int need_dw, int need_dbias);
+
+gdn_status gdn_gated_linear_bwd(const void *dy, const void *x, const void *w, const void *z, void *dx, void *dw,
+                                float *dbias, int M, int N, int K, gdn_dtype dy_dtype, gdn_dtype grad_dtype,
+                                gdn_act act, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * gdn_clock_probe -- measurement aid, not part of the operation: enqueues

@@ -91,3 +91,37 @@ def linear_bwd(dy, x, w, z=None, name="none"):
     """(dx, dw, dbias, dz)."""
     dz = dy if name == "none" else dy * act_grad(name, z)
     return dz @ w, dz.T @ x, dz.sum(axis=0), dz
+
+
+def add_layernorm(x, w, b=None, residual=None, eps=1e-5):
+    """(y, u, mean, rstd)."""
+    u = x if residual is None else x + residual
+    mean = np.mean(u, axis=-1)
+    d = u - mean[..., None]
+    rstd = 1.0 / np.sqrt(np.mean(d * d, axis=-1) + eps)
+    y = d * rstd[..., None] * w
+    return (y if b is None else y + b), u, mean, rstd
+
+
+def add_layernorm_bwd(dy, r, w, mean, rstd, dr=None):
+    """(dx, dw, db) at the given r, mean and rstd."""
+    xhat = (r - mean[..., None]) * rstd[..., None]
+    a = dy * w
+    dx = rstd[..., None] * (a - np.mean(a, axis=-1, keepdims=True) - xhat * np.mean(a * xhat, axis=-1, keepdims=True))
+    D = r.shape[-1]
+    return (dx if dr is None else dx + dr), (dy * xhat).reshape(-1, D).sum(axis=0), dy.reshape(-1, D).sum(axis=0)
+
+
+def gated_linear(x, w, bias=None, name="silu", x_scale=None, w_scale=None):
+    """(y, z): z = (g, u) = (x w^T) x_scale w_scale + bias with the gate's rows of w first, y = act(g) u."""
+    _, z = linear(x, w, bias, None, "none", x_scale, w_scale)
+    N = w.shape[0] // 2
+    return act(name, z[:, :N]) * z[:, N:], z
+
+
+def gated_linear_bwd(dy, x, w, z, name="silu"):
+    """(dx, dw, dbias, dz) with dz = (dg, du)."""
+    N = w.shape[0] // 2
+    g, u = z[:, :N], z[:, N:]
+    dz = np.concatenate([dy * u * act_grad(name, g), dy * act(name, g)], axis=1)
+    return dz @ w, dz.T @ x, dz.sum(axis=0), dz
