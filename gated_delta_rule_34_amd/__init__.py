@@ -23,6 +23,9 @@ __all__ = [
     "gdn_linear_plan", "gdn_linear_bwd_plan",
     "gdn_add_layernorm", "gdn_add_layernorm_bwd", "gdn_add_layernorm_bwd_workspace",
     "gdn_gated_linear", "gdn_gated_linear_workspace", "gdn_gated_linear_bwd", "gdn_gated_linear_bwd_workspace",
+    "gdn_causal_conv", "gdn_causal_conv_varlen",
+    "gdn_selective_scan", "gdn_selective_scan_workspace", "gdn_selective_scan_varlen",
+    "gdn_selective_scan_varlen_workspace", "gdn_selective_step",
     "clock_probe",
     "GDN_F32", "GDN_BF16", "GDN_F8E4M3", "BT",
 ]
@@ -125,6 +128,20 @@ def load():
     lib.gdn_gated_linear_bwd_workspace.argtypes = [_i] * 9
     lib.gdn_gated_linear_bwd.restype = _i
     lib.gdn_gated_linear_bwd.argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
+    lib.gdn_causal_conv.restype = _i
+    lib.gdn_causal_conv.argtypes = [_vp] * 6 + [_i] * 6 + [_vp]
+    lib.gdn_causal_conv_varlen.restype = _i
+    lib.gdn_causal_conv_varlen.argtypes = [_vp] * 7 + [_i] * 6 + [_vp]
+    lib.gdn_selective_scan_workspace.restype = _sz
+    lib.gdn_selective_scan_workspace.argtypes = [_i] * 4
+    lib.gdn_selective_scan.restype = _i
+    lib.gdn_selective_scan.argtypes = [_vp] * 11 + [_i] * 5 + [_vp, _sz, _vp]
+    lib.gdn_selective_scan_varlen_workspace.restype = _sz
+    lib.gdn_selective_scan_varlen_workspace.argtypes = [_i] * 4
+    lib.gdn_selective_scan_varlen.restype = _i
+    lib.gdn_selective_scan_varlen.argtypes = [_vp] * 12 + [_i] * 5 + [_vp, _sz, _vp]
+    lib.gdn_selective_step.restype = _i
+    lib.gdn_selective_step.argtypes = [_vp] * 11 + [_i] * 4 + [_vp]
     _lib = lib
     return lib
 
@@ -1085,6 +1102,166 @@ def gdn_gated_linear_bwd(dy, x, weight, z, act="silu", bias=False, grad_dtype=No
                _addr(dy), _addr(x), _addr(weight), _addr(z), _addr(dx), _addr(dw), _addr(db), M, N, K, dyc, gc, a,
                _addr(ws), nbytes)
     return dx, dw, db
+
+
+def _conv(name, x, weight, cu, seqs, bias, act, conv_state, update_conv_state, out):
+    torch = _torch()
+    dev, f32 = x.device, torch.float32
+    lead, C = tuple(x.shape[:-1]), x.shape[-1]
+    _need(x, "x", lead + (C,), x.dtype, dev)
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [C, W], got {tuple(weight.shape)}")
+    W = weight.shape[1]
+    _need(weight, "weight", (C, W), f32, dev)
+    if bias is not None:
+        _need(bias, "bias", (C,), f32, dev)
+    if conv_state is not None:
+        _need(conv_state, "conv_state", (seqs, W - 1, C), f32, dev)
+    if act not in ("none", "silu"):
+        raise ValueError(f"act must be none or silu, got {act!r}")
+    if update_conv_state:
+        if conv_state is None:
+            raise ValueError("update_conv_state needs conv_state")
+        state = conv_state
+    else:
+        state = torch.empty((seqs, W - 1, C), dtype=f32, device=dev)
+    y = torch.empty_like(x) if out is None else out
+    if out is not None:
+        _need(y, "out", lead + (C,), x.dtype, dev)
+    code = _code(x.dtype, "x")
+    lib = load()
+    if cu is None:
+        _on_device(lib.gdn_causal_conv, name, dev, _addr(x), _addr(weight), _addr(bias), _addr(conv_state), _addr(y),
+                   _addr(state), lead[0], lead[1], C, W, code, _act_code(act))
+    else:
+        _need(cu, "cu_seqlens", (seqs + 1,), torch.int32, dev)
+        _on_device(lib.gdn_causal_conv_varlen, name, dev, _addr(x), _addr(weight), _addr(bias), _addr(cu),
+                   _addr(conv_state), _addr(y), _addr(state), seqs, lead[0], C, W, code, _act_code(act))
+    return y, state
+
+
+def gdn_causal_conv(x, weight, bias=None, act="silu", conv_state=None, update_conv_state=False, out=None):
+    """Short causal convolution per channel: y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}).  x [B,T,C] bf16 or fp32;
+    weight [C,W] fp32, W 2 to 4; bias [C] fp32 or None; act: none or silu; conv_state [B,W-1,C] fp32 (the inputs before
+    t = 0, oldest first) or None.  Returns (y in the type of x, new conv state); with update_conv_state the new state
+    overwrites conv_state.  T = 1 is one decode token."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, T, C], got {tuple(x.shape)}")
+    return _conv("gdn_causal_conv", x, weight, None, x.shape[0], bias, act, conv_state, update_conv_state, out)
+
+
+def gdn_causal_conv_varlen(x, weight, cu_seqlens, bias=None, act="silu", conv_state=None, update_conv_state=False,
+                           out=None):
+    """gdn_causal_conv over packed sequences: x [total_T,C], cu_seqlens int32 [N+1] on the device, states [N,W-1,C]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [total_T, C], got {tuple(x.shape)}")
+    return _conv("gdn_causal_conv_varlen", x, weight, cu_seqlens, cu_seqlens.numel() - 1, bias, act, conv_state,
+                 update_conv_state, out)
+
+
+def gdn_selective_scan_workspace(B, T, ch, N):
+    return int(load().gdn_selective_scan_workspace(B, T, ch, N))
+
+
+def gdn_selective_scan_varlen_workspace(seqs, total_T, ch, N):
+    return int(load().gdn_selective_scan_varlen_workspace(seqs, total_T, ch, N))
+
+
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
+    """Checks what the scan and the step share; (channels, states)."""
+    f32 = _torch().float32
+    dev, lead, ch = x.device, tuple(x.shape[:-1]), x.shape[-1]
+    if A.dim() != 2:
+        raise ValueError(f"A must be [channels, N], got {tuple(A.shape)}")
+    N = A.shape[1]
+    _need(x, "x", lead + (ch,), x.dtype, dev)
+    _need(dt, "dt", lead + (ch,), x.dtype, dev)
+    _need(A, "A", (ch, N), f32, dev)
+    _need(B, "B", lead + (N,), x.dtype, dev)
+    _need(C, "C", lead + (N,), x.dtype, dev)
+    if D is not None:
+        _need(D, "D", (ch,), f32, dev)
+    if z is not None:
+        _need(z, "z", lead + (ch,), x.dtype, dev)
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", (ch,), f32, dev)
+    return ch, N
+
+
+def _scan(name, x, dt, A, B, C, cu, seqs, D, z, dt_bias, h0, output_final_state, workspace, out, final_state):
+    torch = _torch()
+    dev, f32 = x.device, torch.float32
+    ch, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    if h0 is not None:
+        _need(h0, "h0", (seqs, ch, N), f32, dev)
+    y = torch.empty_like(x) if out is None else out
+    if out is not None:
+        _need(y, "out", tuple(x.shape), x.dtype, dev)
+    ht = None
+    if output_final_state:
+        ht = torch.empty((seqs, ch, N), dtype=f32, device=dev) if final_state is None else final_state
+        _need(ht, "final_state", (seqs, ch, N), f32, dev)
+    code = _code(x.dtype, "x")
+    lib = load()
+    T = x.shape[0] if cu is not None else x.shape[1]
+    ws = workspace
+    if ws is None:
+        query = lib.gdn_selective_scan_workspace if cu is None else lib.gdn_selective_scan_varlen_workspace
+        nbytes = query(seqs, T, ch, N)
+        if nbytes:
+            ws = _scratch(nbytes, dev)
+    else:
+        nbytes = _given(ws, dev)
+    if cu is None:
+        _on_device(lib.gdn_selective_scan, name, dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C), _addr(D),
+                   _addr(z), _addr(dt_bias), _addr(h0), _addr(y), _addr(ht), seqs, T, ch, N, code, _addr(ws), nbytes)
+    else:
+        _need(cu, "cu_seqlens", (seqs + 1,), torch.int32, dev)
+        _on_device(lib.gdn_selective_scan_varlen, name, dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+                   _addr(cu), _addr(D), _addr(z), _addr(dt_bias), _addr(h0), _addr(y), _addr(ht), seqs, T, ch, N, code,
+                   _addr(ws), nbytes)
+    return y, ht
+
+
+def gdn_selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, output_final_state=True, workspace=None,
+                       out=None, final_state=None):
+    """Selective state space scan: d = softplus(dt + dt_bias), h_t = exp(d A) h_{t-1} + d x B, y = (C . h + D x) silu(z).
+    x, dt, z [batch,T,ch] and B, C [batch,T,N] in one type (bf16 or fp32); A [ch,N], D, dt_bias [ch] fp32 (z, D and
+    dt_bias may be None); h0 [batch,ch,N] fp32 or None; N 8, 16, 32 or 64.  final_state may be h0 itself.  Returns (y in
+    the type of x, final state or None)."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [batch, T, channels], got {tuple(x.shape)}")
+    return _scan("gdn_selective_scan", x, dt, A, B, C, None, x.shape[0], D, z, dt_bias, h0, output_final_state, workspace,
+                 out, final_state)
+
+
+def gdn_selective_scan_varlen(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, h0=None,
+                              output_final_state=True, workspace=None, out=None, final_state=None):
+    """gdn_selective_scan over packed sequences: x, dt, z [total_T,ch], B, C [total_T,N], cu_seqlens int32 [n+1] on the
+    device, states [n,ch,N]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [total_T, channels], got {tuple(x.shape)}")
+    return _scan("gdn_selective_scan_varlen", x, dt, A, B, C, cu_seqlens, cu_seqlens.numel() - 1, D, z, dt_bias, h0,
+                 output_final_state, workspace, out, final_state)
+
+
+def gdn_selective_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, out=None, state_out=None):
+    """One decode token of gdn_selective_scan: x, dt, z [batch,ch], B, C [batch,N], state [batch,ch,N] fp32, updated in
+    place unless state_out is given.  Returns (y [batch,ch], the new state)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError(f"x must be [batch, channels], got {tuple(x.shape)}")
+    dev, n = x.device, x.shape[0]
+    ch, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    _need(state, "state", (n, ch, N), torch.float32, dev)
+    new = state if state_out is None else state_out
+    _need(new, "state_out", (n, ch, N), torch.float32, dev)
+    y = torch.empty_like(x) if out is None else out
+    if out is not None:
+        _need(y, "out", (n, ch), x.dtype, dev)
+    _on_device(load().gdn_selective_step, "gdn_selective_step", dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+               _addr(D), _addr(z), _addr(dt_bias), _addr(state), _addr(new), _addr(y), n, ch, N, _code(x.dtype, "x"))
+    return y, new
 
 
 def clock_probe(nblocks=256, spin_us=2000, device="cuda"):

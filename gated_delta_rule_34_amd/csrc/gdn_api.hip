@@ -903,4 +903,113 @@ gdn_status gdn_linear_bwd_plan(int M, int N, int K, gdn_dtype dy_dtype, gdn_dtyp
     return GDN_OK;
 }
 
+static gdn_status conv_call(const void *x, const float *w, const float *bias, const int *cu, const float *state_in,
+                            void *y, float *state_out, int seqs, int T, long long total, int C, int W,
+                            gdn_dtype dtype, gdn_act act, void *stream) {
+    if (!x || !w || !y || seqs < 1 || T < 1 || C < 1) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || W < 2 || W > 4 || (act != GDN_ACT_NONE && act != GDN_ACT_SILU)) return GDN_ERR_UNSUPPORTED;
+    const long long octets = ((long long)C + 7) / 8;
+    if (total > (1 << 30) || total * octets >= (1LL << 32) - 256 || seqs * octets >= (1LL << 32) - 256)
+        return GDN_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w, 4) || !aligned(bias, 4) || !aligned(cu, 4) ||
+        !aligned(state_in, 4) || !aligned(state_out, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t n = (size_t)total * C * esize(dtype), ns = (size_t)seqs * (W - 1) * C * 4;
+    const Range ins[] = {{x, n}, {w, (size_t)C * W * 4}, {bias, (size_t)C * 4}, {cu, cu ? (size_t)(seqs + 1) * 4 : 0},
+                         {state_in == state_out ? nullptr : state_in, ns}};
+    const Range outs[] = {{y, n}, {state_out, ns}};
+    if (!disjoint(ins, outs) || overlap({y, n}, {state_in, ns})) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_causal_conv(x, w, bias, state_in, y, state_out, cu, seqs, T, (int)total, C, W,
+                                            dtype == GDN_BF16, act == GDN_ACT_SILU, (hipStream_t)stream));
+}
+
+gdn_status gdn_causal_conv(const void *x, const float *w, const float *bias, const float *state_in, void *y,
+                           float *state_out, int B, int T, int C, int W, gdn_dtype dtype, gdn_act act, void *stream) {
+    return conv_call(x, w, bias, nullptr, state_in, y, state_out, B, T, (long long)B * T, C, W, dtype, act, stream);
+}
+
+gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bias, const int *cu_seqlens,
+                                  const float *state_in, void *y, float *state_out, int N, int total_T, int C, int W,
+                                  gdn_dtype dtype, gdn_act act, void *stream) {
+    if (!cu_seqlens) return GDN_ERR_INVALID_ARG;
+    return conv_call(x, w, bias, cu_seqlens, state_in, y, state_out, N, total_T, total_T, C, W, dtype, act, stream);
+}
+
+// Sizes of a scan: 32-bit token numbers, a grid of fewer than 2^32 threads.
+static gdn_status scan_check(int seqs, int T, long long total, int ch, int N, bool packed) {
+    if (seqs < 1 || T < 1 || ch < 1 || N < 1) return GDN_ERR_INVALID_ARG;
+    if ((N != 8 && N != 16 && N != 32 && N != 64) || total > (1 << 30) || ch > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    const gdn::ScanPlan p = gdn::scan_plan(seqs, T, (int)total, ch, N, packed);
+    return (long long)p.segs * ((ch + 63) / 64) < (1LL << 23) ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+size_t gdn_selective_scan_workspace(int B, int T, int ch, int N) {
+    if (scan_check(B, T, (long long)B * T, ch, N, false) != GDN_OK) return 0;
+    return gdn::scan_plan(B, T, B * T, ch, N, false).total;
+}
+
+size_t gdn_selective_scan_varlen_workspace(int seqs, int total_T, int ch, int N) {
+    if (scan_check(seqs, total_T, total_T, ch, N, true) != GDN_OK) return 0;
+    return gdn::scan_plan(seqs, total_T, total_T, ch, N, true).total;
+}
+
+static gdn_status scan_call(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                            const int *cu, const float *D, const void *z, const float *dt_bias, const float *h0, void *y,
+                            float *ht, int seqs, int T, long long total, int ch, int N, gdn_dtype dtype, void *ws,
+                            size_t ws_bytes, void *stream) {
+    if (!x || !dt || !A || !Bm || !Cm || !y) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return GDN_ERR_UNSUPPORTED;
+    const gdn_status st = scan_check(seqs, T, total, ch, N, cu != nullptr);
+    if (st != GDN_OK) return st;
+    for (const void *p : {x, dt, (const void *)A, Bm, Cm, z, (const void *)h0, (const void *)y, (const void *)ht})
+        if (!aligned(p, 16)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(cu, 4)) return GDN_ERR_INVALID_ARG;
+    const gdn::ScanPlan plan = gdn::scan_plan(seqs, T, (int)total, ch, N, cu != nullptr);
+    const size_t need = plan.total;
+    if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+    const size_t es = esize(dtype), n = (size_t)total * ch * es, nb = (size_t)total * N * es;
+    const size_t ns = (size_t)seqs * ch * N * 4;
+    const Range ins[] = {{x, n}, {dt, n}, {A, (size_t)ch * N * 4}, {Bm, nb}, {Cm, nb}, {D, (size_t)ch * 4}, {z, n},
+                         {dt_bias, (size_t)ch * 4}, {cu, cu ? (size_t)(seqs + 1) * 4 : 0},
+                         {h0 == ht ? nullptr : h0, ns}};
+    const Range outs[] = {{y, n}, {ht, ns}, {need ? ws : nullptr, need}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_selective_scan(plan, x, dt, A, Bm, Cm, D, z, dt_bias, h0, y, ht, cu, seqs, T, (int)total,
+                                               ch, N, dtype == GDN_BF16, (char *)ws, (hipStream_t)stream));
+}
+
+gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                              const float *D, const void *z, const float *dt_bias, const float *h0, void *y, float *ht,
+                              int B, int T, int ch, int N, gdn_dtype dtype, void *ws, size_t ws_bytes, void *stream) {
+    return scan_call(x, dt, A, Bm, Cm, nullptr, D, z, dt_bias, h0, y, ht, B, T, (long long)B * T, ch, N, dtype, ws,
+                     ws_bytes, stream);
+}
+
+gdn_status gdn_selective_scan_varlen(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                     const int *cu_seqlens, const float *D, const void *z, const float *dt_bias,
+                                     const float *h0, void *y, float *ht, int seqs, int total_T, int ch, int N,
+                                     gdn_dtype dtype, void *ws, size_t ws_bytes, void *stream) {
+    if (!cu_seqlens) return GDN_ERR_INVALID_ARG;
+    return scan_call(x, dt, A, Bm, Cm, cu_seqlens, D, z, dt_bias, h0, y, ht, seqs, total_T, total_T, ch, N, dtype, ws,
+                     ws_bytes, stream);
+}
+
+gdn_status gdn_selective_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                              const float *D, const void *z, const float *dt_bias, const float *h_in, float *h_out,
+                              void *y, int B, int ch, int N, gdn_dtype dtype, void *stream) {
+    if (!x || !dt || !A || !Bm || !Cm || !h_in || !h_out || !y || B < 1 || ch < 1 || N < 1) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || (N != 8 && N != 16 && N != 32 && N != 64)) return GDN_ERR_UNSUPPORTED;
+    if ((long long)B * ch >= ((1LL << 32) - 256) / (N / 4)) return GDN_ERR_UNSUPPORTED;
+    for (const void *p : {x, dt, (const void *)A, Bm, Cm, z, (const void *)h_in, (const void *)h_out, (const void *)y})
+        if (!aligned(p, 16)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(D, 4) || !aligned(dt_bias, 4)) return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(dtype), n = (size_t)B * ch * es, nb = (size_t)B * N * es, ns = (size_t)B * ch * N * 4;
+    const Range ins[] = {{x, n}, {dt, n}, {A, (size_t)ch * N * 4}, {Bm, nb}, {Cm, nb}, {D, (size_t)ch * 4}, {z, n},
+                         {dt_bias, (size_t)ch * 4}, {h_in == h_out ? nullptr : h_in, ns}};
+    const Range outs[] = {{y, n}, {h_out, ns}};
+    if (!disjoint(ins, outs)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_selective_step(x, dt, A, Bm, Cm, D, z, dt_bias, h_in, h_out, y, B, ch, N,
+                                               dtype == GDN_BF16, (hipStream_t)stream));
+}
+
 }  // extern "C"

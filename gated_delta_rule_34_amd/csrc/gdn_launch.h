@@ -208,4 +208,25 @@ hipError_t launch_add_layernorm_bwd(const void *dy, const void *r, const float *
                                     const float *rstd, const void *dr, void *dx, float *dw, float *db, float *part,
                                     long rows, int D, bool dy_bf16, bool r_bf16, hipStream_t st);
 
+// The selective scan and its convolution (gdn_scan.hip).  cu (nullable): seqs
+// sequences packed into total tokens, else seqs of T tokens; bf16 or fp32.
+hipError_t launch_causal_conv(const void *x, const float *w, const float *bias, const float *state_in, void *y,
+                              float *state_out, const int *cu, int seqs, int T, int total, int C, int W, bool bf16,
+                              bool silu, hipStream_t st);
+// How a scan is cut along its tokens: segments of L tokens, per_seq to a
+// sequence (packed: to all tokens), and the offsets of what passes between
+// them (total 0: one segment each, nothing does).
+struct ScanPlan {
+    int L, per_seq, segs;
+    size_t f_off, h_off, total;
+};
+ScanPlan scan_plan(int seqs, int T, int total, int ch, int N, bool packed);
+hipError_t launch_selective_scan(const ScanPlan &p, const void *x, const void *dt, const float *A, const void *B,
+                                 const void *C, const float *D, const void *z, const float *dt_bias, const float *h0,
+                                 void *y, float *ht, const int *cu, int seqs, int T, int total, int ch, int N, bool bf16,
+                                 char *ws, hipStream_t st);
+hipError_t launch_selective_step(const void *x, const void *dt, const float *A, const void *B, const void *C,
+                                 const float *D, const void *z, const float *dt_bias, const float *h0, float *h1,
+                                 void *y, int seqs, int ch, int N, bool bf16, hipStream_t st);
+
 }  // namespace gdn

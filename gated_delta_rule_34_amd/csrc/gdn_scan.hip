@@ -1,0 +1,671 @@
+// gdn_scan.hip -- the selective state space scan and the short causal
+// convolution in front of it.
+//   convolution  y_t = act(b + sum_j w_j x_{t-W+1+j}) per channel
+//   scan         d = softplus(dt + dt_bias), per channel and state n
+//                h_n = exp(d A_n) h_n + d x B_n
+//                y = (sum_n C_n h_n + D x) silu(z)
+// The decay differs in every channel and state, so there is no matrix product
+// in it: a state costs one exponential, two products and two multiply-adds a
+// token, on the vector unit.
+#include "gdn_device.h"
+#include "gdn_launch.h"
+#include "gdn_row.h"
+#include "gdn_tile.h"
+
+namespace gdn {
+
+__device__ __forceinline__ float silu_of(float z) {
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z * LOG2E));
+}
+
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|).  log1p(e) = 2 atanh(s)
+// with s = e / (2 + e) <= 1/3, by its odd series to s^15 (the next term is
+// 2e-9): small steps keep their relative accuracy, which the logarithm of
+// 1 + e would lose.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = __builtin_amdgcn_exp2f(-fabsf(v) * LOG2E);
+    const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
+    float p = 1.f / 15.f;
+    p = fmaf(p, q, 1.f / 13.f);
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    p = fmaf(p, q, 1.f);
+    return (v > 0.f ? v : 0.f) + 2.f * s * p;
+}
+
+// Sequence offsets, clamped so that malformed ones stay in range.
+__device__ __forceinline__ int seq_at(const int *cu, int n, int total) { return min(max(cu[n], 0), total); }
+
+// ---- the convolution ------------------------------------------------------------
+
+struct ConvArgs {
+    const void *x;
+    const float *w, *bias, *state_in;
+    void *y;
+    float *state_out;   // null where the state is written by conv_state_kernel
+    const int *cu;      // null: seqs sequences of T tokens
+    int seqs, T, total; // total: tokens
+    int C, octets;
+    int run;            // tokens a thread walks
+    int runs;           // runs of a sequence (dense) or of all tokens (packed)
+    bool silu;
+};
+
+// A thread owns eight channels over a run of tokens: the window slides through
+// its registers, every input is read once a run (and W - 1 before it again).
+// Four tokens' loads are in flight at a time.
+template <class ET, int W>
+__global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
+    constexpr int AT = 4, H = W - 1;
+    const long id = (long)blockIdx.x * 256 + threadIdx.x;
+    const long u = id / a.octets;
+    const int c = (int)(id - u * a.octets) * 8;
+    int n, start, end, t0, t1;
+    if (a.cu) {
+        if (u >= a.runs) return;
+        t0 = (int)u * a.run;
+        t1 = min(t0 + a.run, a.total);
+        int lo = 0, hi = a.seqs;  // the first sequence that ends behind t0
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (seq_at(a.cu, mid + 1, a.total) > t0) hi = mid;
+            else lo = mid + 1;
+        }
+        n = lo - 1;
+        start = end = t0;         // the walk below enters sequence lo
+        if (a.state_out) {  // sequences without tokens, shared among the runs
+            for (int k = (int)u; k < a.seqs; k += a.runs) {
+                if (seq_at(a.cu, k + 1, a.total) > seq_at(a.cu, k, a.total)) continue;
+                for (int j = 0; j < H; ++j) {
+                    const long at = ((long)k * H + j) * a.C;
+                    const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    store8v(a.state_out + at, a.state_in ? load8v(a.state_in + at, c, a.C) : zero, c, a.C);
+                }
+            }
+        }
+    } else {
+        n = (int)(u / a.runs);
+        if (n >= a.seqs) return;
+        start = n * a.T;
+        end = start + a.T;
+        t0 = start + (int)(u - (long)n * a.runs) * a.run;
+        t1 = min(t0 + a.run, end);
+    }
+    const ET *x = (const ET *)a.x;
+    ET *y = (ET *)a.y;
+    float w[8][W];
+    f32x8 bias;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        bias[e] = a.bias && c + e < a.C ? a.bias[c + e] : 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[e][j] = c + e < a.C ? a.w[(long)(c + e) * W + j] : 0.f;
+    }
+    f32x8 hist[H];  // the H inputs before t, oldest first
+    auto enter = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int p = t - H + j;
+            if (p >= start) hist[j] = raw_f32(load_raw(x + (long)p * a.C, c, a.C));
+            else if (a.state_in) hist[j] = load8v(a.state_in + ((long)n * H + (p - start + H)) * a.C, c, a.C);
+            else hist[j] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        }
+    };
+    bool in = false;  // hist holds what comes before t
+    for (int t = t0; t < t1; t += AT) {
+        typename RawOf<ET>::type raw[AT];
+#pragma unroll
+        for (int k = 0; k < AT; ++k) raw[k] = load_raw(x + (long)min(t + k, t1 - 1) * a.C, c, a.C);
+#pragma unroll
+        for (int k = 0; k < AT; ++k) {
+            const int now = t + k;
+            if (now >= t1) break;
+            if (a.cu && now >= end) {  // on to the sequence of this token
+                do {
+                    ++n;
+                    if (n >= a.seqs) return;  // behind the last one
+                    start = seq_at(a.cu, n, a.total);
+                    end = seq_at(a.cu, n + 1, a.total);
+                } while (end <= now);
+                in = false;
+            }
+            if (now < start) continue;
+            if (!in) enter(now);
+            in = true;
+            const f32x8 v = raw_f32(raw[k]);
+            f32x8 o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float s = bias[e];
+#pragma unroll
+                for (int j = 0; j < H; ++j) s = fmaf(w[e][j], hist[j][e], s);
+                s = fmaf(w[e][H], v[e], s);
+                o[e] = a.silu ? silu_of(s) : s;
+            }
+            store8v(y + (long)now * a.C, o, c, a.C);
+#pragma unroll
+            for (int j = 0; j + 1 < H; ++j) hist[j] = hist[j + 1];
+            hist[H - 1] = v;
+            if (now + 1 == end && a.state_out) {
+#pragma unroll
+                for (int j = 0; j < H; ++j) store8v(a.state_out + ((long)n * H + j) * a.C, hist[j], c, a.C);
+            }
+        }
+    }
+}
+
+// The carried inputs after each sequence, in place: a thread reads all that its
+// eight channels need before it writes them.
+template <class ET, int W>
+__global__ __launch_bounds__(256) void conv_state_kernel(ConvArgs a, float *out) {
+    constexpr int H = W - 1;
+    const long id = (long)blockIdx.x * 256 + threadIdx.x;
+    const int n = (int)(id / a.octets), c = (int)(id - (long)n * a.octets) * 8;
+    if (n >= a.seqs) return;
+    const int start = a.cu ? seq_at(a.cu, n, a.total) : n * a.T;
+    const int end = a.cu ? max(seq_at(a.cu, n + 1, a.total), start) : start + a.T;
+    f32x8 hist[H];
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+        const int p = end - H + j;
+        if (p >= start) hist[j] = raw_f32(load_raw((const ET *)a.x + (long)p * a.C, c, a.C));
+        else hist[j] = load8v(a.state_in + ((long)n * H + (p - start + H)) * a.C, c, a.C);
+    }
+#pragma unroll
+    for (int j = 0; j < H; ++j) store8v(out + ((long)n * H + j) * a.C, hist[j], c, a.C);
+}
+
+template <class ET, int W>
+static hipError_t conv_run(ConvArgs a, float *state_out, bool apart, hipStream_t st) {
+    a.state_out = apart ? nullptr : state_out;
+    const long threads = (long)(a.cu ? 1 : a.seqs) * a.runs * a.octets;
+    hipLaunchKernelGGL((conv_kernel<ET, W>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !apart || !state_out) return e;
+    const long n = (long)a.seqs * a.octets;
+    hipLaunchKernelGGL((conv_state_kernel<ET, W>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a, state_out);
+    return hipGetLastError();
+}
+
+hipError_t launch_causal_conv(const void *x, const float *w, const float *bias, const float *state_in, void *y,
+                              float *state_out, const int *cu, int seqs, int T, int total, int C, int W, bool bf16,
+                              bool silu, hipStream_t st) {
+    ConvArgs a{x, w, bias, state_in, y, nullptr, cu, seqs, T, total, C, (C + 7) / 8, 0, 0, silu};
+    const int per = cu ? total : T;
+    a.run = 16;
+    while (a.run > 4 && (long)total * a.octets / a.run < 64 * 2048) a.run /= 2;
+    a.runs = (per + a.run - 1) / a.run;
+    // in place, a run at a sequence's end would overwrite what one at its start reads
+    const bool apart = state_in && state_in == state_out && (cu || T > a.run);
+#define GDN_CONV(Wv)                                                              \
+    if (W == Wv)                                                                  \
+        return bf16 ? conv_run<uint16_t, Wv>(a, state_out, apart, st) : conv_run<float, Wv>(a, state_out, apart, st);
+    GDN_CONV(2)
+    GDN_CONV(3)
+    GDN_CONV(4)
+#undef GDN_CONV
+    return hipErrorInvalidValue;
+}
+
+// ---- the scan -------------------------------------------------------------------
+
+// Four consecutive values of a row of D as they lie in memory, zero past its end.
+template <class ET> struct Four;
+template <> struct Four<uint16_t> {
+    uint2 u;
+    __device__ __forceinline__ void load(const uint16_t *p, int c, int D) {
+        typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
+        if (c + 4 <= D) {
+            const v2 t = *(const v2 *)(p + c);
+            u = make_uint2(t[0], t[1]);
+        } else {
+            uint32_t t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = c + e < D ? p[c + e] : 0;
+            u = make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
+        }
+    }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+    __device__ __forceinline__ float operator[](int e) const {
+        const uint32_t v = e < 2 ? u.x : u.y;
+        return __uint_as_float(e & 1 ? v & 0xffff0000u : v << 16);
+    }
+    static __device__ __forceinline__ void store(uint16_t *p, const f32x4 &v, int c, int D) {
+        typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
+        if (c + 4 <= D) {
+            *(v2 *)(p + c) = v2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < D) p[c + e] = to_bf16(v[e]);
+        }
+    }
+};
+template <> struct Four<float> {
+    f32x4 u;
+    __device__ __forceinline__ void load(const float *p, int c, int D) {
+        if (c + 4 <= D) {
+            u = *(const f32x4_a4 *)(p + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = c + e < D ? p[c + e] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void zero() { u = f32x4{0.f, 0.f, 0.f, 0.f}; }
+    __device__ __forceinline__ float operator[](int e) const { return u[e]; }
+    static __device__ __forceinline__ void store(float *p, const f32x4 &v, int c, int D) {
+        if (c + 4 <= D) {
+            *(f32x4_a4 *)(p + c) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < D) p[c + e] = v[e];
+        }
+    }
+};
+
+constexpr int kTT = 16;   // tokens a tile
+constexpr int kCH = 64;   // channels a workgroup
+
+struct ScanArgs {
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *dt_bias, *h0;
+    void *y;
+    float *ht;
+    const int *cu;         // null: seqs sequences of T tokens
+    int seqs, T, total;
+    int ch, L;             // channels; tokens a segment
+    int per_seq;           // dense: segments a sequence
+    float *E, *F;          // [segment, ch, N] state at a segment's end from zero (or its sequence's start); [segment, ch] sum of d
+};
+
+struct Tile {
+    int t, len, seq;  // first token, tokens (0: none left), sequence
+    bool first, last; // it begins, ends its sequence
+};
+
+// Tiles of a segment in order, none across a sequence's end.  Every wave of a
+// workgroup walks the same ones.
+struct Walk {
+    int pos, n, start, end, stop;
+    __device__ __forceinline__ void init(const ScanArgs &a, int seg, int lane) {
+        if (a.cu) {
+            pos = seg * a.L;
+            stop = min(pos + a.L, a.total);
+            n = 0;  // sequences that end at or before pos
+            for (int k = 0; k < a.seqs; k += 64) {
+                const bool before = k + lane < a.seqs && seq_at(a.cu, k + lane + 1, a.total) <= pos;
+                n += __popcll(__ballot(before));
+            }
+            n = __builtin_amdgcn_readfirstlane(n);
+            bounds(a);
+        } else {
+            n = seg / a.per_seq;
+            start = n * a.T;
+            end = start + a.T;
+            pos = start + (seg - n * a.per_seq) * a.L;
+            stop = min(pos + a.L, end);
+        }
+    }
+    __device__ __forceinline__ void bounds(const ScanArgs &a) {
+        if (n < a.seqs) {
+            start = __builtin_amdgcn_readfirstlane(seq_at(a.cu, n, a.total));
+            end = __builtin_amdgcn_readfirstlane(seq_at(a.cu, n + 1, a.total));
+        } else {
+            start = end = stop;
+        }
+    }
+    // The tile at pos; moves on.
+    __device__ __forceinline__ Tile next(const ScanArgs &a) {
+        Tile r{0, 0, 0, false, false};
+        if (a.cu) {
+            while (pos >= end && n < a.seqs) {
+                ++n;
+                bounds(a);
+            }
+            if (n >= a.seqs) return r;
+            pos = max(pos, start);
+        }
+        if (pos >= stop) return r;
+        r.t = pos;
+        r.seq = n;
+        r.len = min(min(kTT, end - pos), stop - pos);
+        r.first = pos == start;
+        pos += r.len;
+        r.last = pos == end;
+        return r;
+    }
+};
+
+// A workgroup owns 64 channels of a segment.  Four waves scan: a lane holds a
+// quarter of a channel's states, so that what a token costs them is its
+// arithmetic and four LDS accesses, and leaves its part of y in LDS.  Four
+// waves work beside them, a tile ahead and a tile behind: they load x, dt, z, B
+// and C (two tiles ahead), compute d and d x once per token and channel, and
+// turn the parts of y into outputs.  One barrier a tile.
+// CARRY: only the state at the segment's end, and the sum of d, for the
+// segments that follow (E, F); with several segments a sequence's state enters
+// a segment as E of the last, plus exp(A F) times what entered that, and so on
+// back to the segment where the sequence starts.
+template <class ET, int N, bool CARRY>
+__global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
+    constexpr int SPL = N / 4, PB = N / 8;
+    typedef float sv __attribute__((ext_vector_type(SPL)));
+    __shared__ __attribute__((aligned(16))) float2 dd[2][kTT][kCH];
+    __shared__ __attribute__((aligned(16))) float bc[2][2][kTT][N];
+    __shared__ __attribute__((aligned(16))) float part[CARRY ? 1 : 2][CARRY ? 1 : kTT][4][kCH];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int groups = (a.ch + kCH - 1) / kCH, seg = blockIdx.x / groups, c0 = (blockIdx.x % groups) * kCH;
+    Walk walk;
+    walk.init(a, seg, lane);
+    if constexpr (CARRY) {
+        // needed only where the sequence of the last token goes on; from its start
+        if (a.cu) {
+            Walk end = walk;
+            end.pos = walk.stop - 1;
+            while (end.pos >= end.end && end.n < a.seqs) {
+                ++end.n;
+                end.bounds(a);
+            }
+            if (end.n >= a.seqs || end.end <= walk.stop) return;
+            walk.n = end.n;
+            walk.start = end.start;
+            walk.end = end.end;
+            walk.pos = max(walk.pos, end.start);
+        } else if (walk.stop == walk.end) {
+            return;
+        }
+    }
+    if (wave < 4) {
+        const int c = c0 + lane, n0 = wave * SPL;
+        const bool live = c < a.ch;
+        sv A, h;
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+            A[s] = live ? a.A[(long)c * N + n0 + s] * LOG2E : 0.f;
+            h[s] = 0.f;
+        }
+        float sum = 0.f;
+        if (!CARRY) {
+            if (a.cu && a.ht) {  // sequences without tokens pass their state on
+                for (int k = seg * 64; k < a.seqs; k += gridDim.x / groups * 64) {
+                    const bool none = k + lane < a.seqs &&
+                                      seq_at(a.cu, k + lane + 1, a.total) <= seq_at(a.cu, k + lane, a.total);
+                    for (uint64_t m = __ballot(none); m; m &= m - 1) {
+                        const long at = ((long)(k + __builtin_ctzll(m)) * a.ch + c) * N + n0;
+                        sv v;
+#pragma unroll
+                        for (int s = 0; s < SPL; ++s) v[s] = 0.f;
+                        if (live && a.h0) v = *(const sv *)(a.h0 + at);
+                        if (live) *(sv *)(a.ht + at) = v;
+                    }
+                }
+            }
+            if (walk.pos > walk.start && walk.n < a.seqs) {  // the sequence comes from segments before
+                const int q0 = a.cu ? walk.start / a.L : walk.n * a.per_seq;
+                if (live)
+                    for (int q = q0; q < seg; ++q) {
+                        const sv e = *(const sv *)(a.E + ((long)q * a.ch + c) * N + n0);
+                        const float f = a.F[(long)q * a.ch + c];
+#pragma unroll
+                        for (int s = 0; s < SPL; ++s)
+                            h[s] = q == q0 ? e[s] : fmaf(__builtin_amdgcn_exp2f(f * A[s]), h[s], e[s]);
+                    }
+            }
+        }
+        __syncthreads();
+        for (int buf = 0;; buf ^= 1) {
+            const Tile tile = walk.next(a);
+            if (tile.len == 0) break;
+            if (tile.first) {
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) h[s] = 0.f;
+                if (a.h0 && live) h = *(const sv *)(a.h0 + ((long)tile.seq * a.ch + c) * N + n0);
+            }
+            auto token = [&](int k) {
+                const float2 d = dd[buf][k][lane];
+                const sv b = *(const sv *)&bc[buf][0][k][n0];
+                if (CARRY) sum += d.x;
+                sv cv;
+                if (!CARRY) cv = *(const sv *)&bc[buf][1][k][n0];
+                float y = 0.f;
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    h[s] = fmaf(__builtin_amdgcn_exp2f(d.x * A[s]), h[s], d.y * b[s]);
+                    if (!CARRY) y = s ? fmaf(cv[s], h[s], y) : cv[s] * h[s];
+                }
+                if (!CARRY) part[buf][k][wave][lane] = y;
+            };
+            if (tile.len == kTT) {
+#pragma unroll
+                for (int k = 0; k < kTT; ++k) token(k);
+            } else {
+                for (int k = 0; k < tile.len; ++k) token(k);
+            }
+            if (!CARRY && tile.last && a.ht && live) *(sv *)(a.ht + ((long)tile.seq * a.ch + c) * N + n0) = h;
+            __syncthreads();
+        }
+        if constexpr (CARRY) {
+            if (live) {
+                *(sv *)(a.E + ((long)seg * a.ch + c) * N + n0) = h;
+                if (wave == 0) a.F[(long)seg * a.ch + c] = sum;
+            }
+        } else {
+            __syncthreads();
+        }
+    } else {
+        const int id = threadIdx.x - 256, k = id >> 4, cc = (id & 15) * 4, c = c0 + cc;
+        const int side = id >> 7, bt = (id & 127) * PB / N, bn = (id & 127) * PB % N;
+        f32x4 bias, skip;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bias[e] = a.dt_bias && c + e < a.ch ? a.dt_bias[c + e] : 0.f;
+            skip[e] = a.D && c + e < a.ch ? a.D[c + e] : 0.f;
+        }
+        struct In {
+            Four<ET> x, dt, z;
+            ET b[PB];
+            int t, len;
+        };
+        auto load = [&](In &in) {
+            const Tile tile = walk.next(a);
+            in.t = tile.t;
+            in.len = tile.len;
+            in.x.zero();
+            in.dt.zero();
+            in.z.zero();
+            if (k < in.len) {
+                const long row = (long)(in.t + k) * a.ch;
+                in.x.load((const ET *)a.x + row, c, a.ch);
+                in.dt.load((const ET *)a.dt + row, c, a.ch);
+                if (!CARRY && a.z) in.z.load((const ET *)a.z + row, c, a.ch);
+            }
+            const ET *p = (const ET *)(side ? a.C : a.B) + (long)(in.t + bt) * N + bn;
+#pragma unroll
+            for (int e = 0; e < PB; ++e) in.b[e] = bt < in.len ? p[e] : (ET)0;
+        };
+        auto stage = [&](const In &in, int buf) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float d0 = softplus(in.dt[e] + bias[e]), d1 = softplus(in.dt[e + 1] + bias[e + 1]);
+                *(f32x4 *)&dd[buf][k][cc + e] = f32x4{d0, d0 * in.x[e], d1, d1 * in.x[e + 1]};
+            }
+#pragma unroll
+            for (int e = 0; e < PB; ++e) bc[buf][side][bt][bn + e] = load_elem(&in.b[e]);
+        };
+        auto finish = [&](const In &in, int buf) {
+            if (k >= in.len) return;
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v += *(const f32x4 *)&part[buf][k][w][cc];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = fmaf(skip[e], in.x[e], v[e]);
+                if (a.z) v[e] *= silu_of(in.z[e]);
+            }
+            Four<ET>::store((ET *)a.y + (long)(in.t + k) * a.ch, v, c, a.ch);
+        };
+        In before, now, after, far;
+        now.len = 0;
+        load(after);
+        load(far);
+        stage(after, 0);
+        __syncthreads();
+        for (int buf = 0;; buf ^= 1) {
+            before = now;
+            now = after;
+            after = far;
+            if (now.len == 0) {
+                if constexpr (!CARRY) {
+                    if (before.len) finish(before, buf ^ 1);
+                    __syncthreads();
+                }
+                break;
+            }
+            load(far);
+            if constexpr (!CARRY) {
+                if (before.len) finish(before, buf ^ 1);
+            }
+            if (after.len) stage(after, buf ^ 1);
+            __syncthreads();
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void scan_copy_kernel(const float *src, float *dst, long n) {
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) dst[i] = src[i];
+}
+
+// How a scan is cut along its tokens: enough segments to give each compute
+// unit work.
+ScanPlan scan_plan(int seqs, int T, int total, int ch, int N, bool packed) {
+    const long groups = (ch + kCH - 1) / kCH;
+    ScanPlan p{};
+    const long base = packed ? groups : groups * seqs;
+    const long len = packed ? total : T;
+    long k = base >= 256 ? 1 : (512 + base - 1) / base;
+    const long most = (len + 63) / 64;
+    if (k > most) k = most;
+    long L = (len + k - 1) / k;
+    L = (L + kTT - 1) / kTT * kTT;
+    p.L = (int)L;
+    p.per_seq = (int)((len + L - 1) / L);
+    p.segs = packed ? p.per_seq : p.per_seq * seqs;
+    if (p.per_seq > 1) {
+        auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+        p.f_off = up((size_t)p.segs * ch * N * 4);
+        p.h_off = p.f_off + up((size_t)p.segs * ch * 4);
+        p.total = p.h_off + up((size_t)seqs * ch * N * 4);
+    }
+    return p;
+}
+
+template <class ET, int N>
+static hipError_t scan_run(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
+    const dim3 grid((unsigned)((a.ch + kCH - 1) / kCH) * (unsigned)p.segs);
+    if (p.per_seq > 1) {
+        hipLaunchKernelGGL((scan_kernel<ET, N, true>), grid, dim3(512), 0, st, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((scan_kernel<ET, N, false>), grid, dim3(512), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_selective_scan(const ScanPlan &p, const void *x, const void *dt, const float *A, const void *B,
+                                 const void *C, const float *D, const void *z, const float *dt_bias, const float *h0,
+                                 void *y, float *ht, const int *cu, int seqs, int T, int total, int ch, int N, bool bf16,
+                                 char *ws, hipStream_t st) {
+    ScanArgs a{x, dt, B, C, z, A, D, dt_bias, h0, y, ht, cu, seqs, T, total, ch, p.L, p.per_seq, nullptr, nullptr};
+    if (p.per_seq > 1) {
+        a.E = (float *)ws;
+        a.F = (float *)(ws + p.f_off);
+        if (h0 && h0 == ht) {  // a segment at a sequence's end would overwrite what one at its start reads
+            const long n = (long)seqs * ch * N, blocks = (n + 255) / 256;
+            float *copy = (float *)(ws + p.h_off);
+            hipLaunchKernelGGL(scan_copy_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, st, h0, copy,
+                               n);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            a.h0 = copy;
+        }
+    }
+#define GDN_SCAN(Nv) \
+    if (N == Nv) return bf16 ? scan_run<uint16_t, Nv>(a, p, st) : scan_run<float, Nv>(a, p, st);
+    GDN_SCAN(8)
+    GDN_SCAN(16)
+    GDN_SCAN(32)
+    GDN_SCAN(64)
+#undef GDN_SCAN
+    return hipErrorInvalidValue;
+}
+
+// ---- one token --------------------------------------------------------------------
+
+// A lane holds four states of a channel (16 bytes in, 16 out), N / 4 lanes a
+// channel; y is summed over them on DPP.  Bound by the states' traffic.
+template <class ET, int N>
+__global__ __launch_bounds__(256) void scan_step_kernel(const ET *x, const ET *dt, const float *A, const ET *B,
+                                                        const ET *C, const float *D, const ET *z,
+                                                        const float *dt_bias, const float *h0, float *h1, ET *y,
+                                                        int seqs, int ch) {
+    constexpr int LPC = N / 4;
+    const long id = (long)blockIdx.x * 256 + threadIdx.x;
+    const long u = id / LPC;  // (sequence, channel)
+    const int q = (int)(id % LPC) * 4;
+    if (u >= (long)seqs * ch) return;  // whole groups of LPC lanes
+    const long b = u / ch;
+    const int c = (int)(u - b * ch);
+    const f32x4 h = *(const f32x4 *)(h0 + u * N + q);
+    const f32x4 A4 = *(const f32x4 *)(A + (long)c * N + q);
+    Four<ET> bv, cv;
+    bv.load(B + b * N, q, N);
+    cv.load(C + b * N, q, N);
+    const float xv = load_elem(x + u);
+    const float d = softplus(load_elem(dt + u) + (dt_bias ? dt_bias[c] : 0.f));
+    f32x4 o;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        o[e] = fmaf(__builtin_amdgcn_exp2f(d * LOG2E * A4[e]), h[e], d * xv * bv[e]);
+        s = fmaf(cv[e], o[e], s);
+    }
+    *(f32x4 *)(h1 + u * N + q) = o;
+    s += dpp_f32<0xB1, 0xf>(s);                      // quad_perm [1, 0, 3, 2]
+    if (LPC >= 4) s += dpp_f32<0x4E, 0xf>(s);        // quad_perm [2, 3, 0, 1]
+    if (LPC >= 8) s += dpp_f32<0x141, 0xf>(s);       // row_half_mirror
+    if (LPC >= 16) s += dpp_f32<0x140, 0xf>(s);      // row_mirror
+    if (q == 0) {
+        if (D) s = fmaf(D[c], xv, s);
+        if (z) s *= silu_of(load_elem(z + u));
+        store_elem(y + u, s);
+    }
+}
+
+hipError_t launch_selective_step(const void *x, const void *dt, const float *A, const void *B, const void *C,
+                                 const float *D, const void *z, const float *dt_bias, const float *h0, float *h1,
+                                 void *y, int seqs, int ch, int N, bool bf16, hipStream_t st) {
+    const long threads = (long)seqs * ch * (N / 4);
+    const dim3 grid((unsigned)((threads + 255) / 256));
+#define GDN_STEP(ET, Nv)                                                                                            \
+    hipLaunchKernelGGL((scan_step_kernel<ET, Nv>), grid, dim3(256), 0, st, (const ET *)x, (const ET *)dt, A,        \
+                       (const ET *)B, (const ET *)C, D, (const ET *)z, dt_bias, h0, h1, (ET *)y, seqs, ch)
+#define GDN_STEP_N(Nv)                      \
+    if (N == Nv) {                          \
+        if (bf16) GDN_STEP(uint16_t, Nv);   \
+        else GDN_STEP(float, Nv);           \
+        return hipGetLastError();           \
+    }
+    GDN_STEP_N(8)
+    GDN_STEP_N(16)
+    GDN_STEP_N(32)
+    GDN_STEP_N(64)
+#undef GDN_STEP_N
+#undef GDN_STEP
+    return hipErrorInvalidValue;
+}
+
+}  // namespace gdn

@@ -603,6 +603,81 @@ gdn_status gdn_gated_linear_bwd(const void *dy, const void *x, const void *w, co
                                 gdn_act act, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * gdn_causal_conv -- the short causal convolution in front of a recurrent
+ * mixer, on its own (gdn_prologue holds the delta rule's):
+ *   y_t[c] = act(bias[c] + sum_{j=0..W-1} w[c][j] x_{t-W+1+j}[c])
+ * Before a sequence's first token it reads the carried inputs (zeros when NULL).
+ *   x, y   [B, T, C] dtype (GDN_F32 or GDN_BF16)
+ *   w      [C, W] fp32, W = 2, 3 or 4;  bias [C] fp32, nullable
+ *   state_in   [B, W-1, C] fp32, nullable: the W-1 inputs before t = 0, oldest
+ *              first
+ *   state_out  same layout, nullable: the W-1 inputs that end at the last
+ *              token; may be state_in itself (updated in place)
+ *   act    GDN_ACT_NONE or GDN_ACT_SILU
+ * T = 1 with a state is one decode token.  C any value; B * T * C / 8 below
+ * 2^32.  x and y 16-byte aligned, the others 4-byte.
+ * gdn_causal_conv_varlen: the same on N packed sequences, x, y [total_T, C] and
+ * states [N, W-1, C]; cu_seqlens as in gdn_chunk_fwd_varlen (an empty sequence
+ * passes its state on; tokens that belong to no sequence are left alone).
+ * Errors: GDN_ERR_INVALID_ARG (null required pointers, sizes < 1, misalignment,
+ * an output that overlaps an input or another output), GDN_ERR_UNSUPPORTED (W,
+ * types or activation not listed, sizes beyond the limit), GDN_ERR_HIP.
+ * Asynchronous on `stream`; no workspace.
+ */
+gdn_status gdn_causal_conv(const void *x, const float *w, const float *bias, const float *state_in, void *y,
+                           float *state_out, int B, int T, int C, int W, gdn_dtype dtype, gdn_act act, void *stream);
+gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bias, const int *cu_seqlens,
+                                  const float *state_in, void *y, float *state_out, int N, int total_T, int C, int W,
+                                  gdn_dtype dtype, gdn_act act, void *stream);
+
+/*
+ * gdn_selective_scan -- selective state space scan: a recurrent mixer whose
+ * decay differs in every channel c and state n and depends on the token,
+ *   d_t[c] = softplus(dt_t[c] + dt_bias[c])
+ *   h_t[c][n] = exp(d_t[c] A[c][n]) h_{t-1}[c][n] + d_t[c] x_t[c] B_t[n]
+ *   y_t[c] = (sum_n C_t[n] h_t[c][n] + D[c] x_t[c]) silu(z_t[c])
+ *   x, dt, z, y  [B, T, ch] dtype (GDN_F32 or GDN_BF16); z nullable (no gate)
+ *   Bm, Cm       [B, T, N] dtype, N = 8, 16, 32 or 64
+ *   A            [ch, N] fp32 (negative);  D, dt_bias [ch] fp32, nullable
+ *   h0           [B, ch, N] fp32, nullable (zeros)
+ *   ht           same, nullable: the state after the last token; may alias h0
+ *                exactly
+ * fp32 arithmetic and states, one rounding per output.  Few sequences of few
+ * channels are cut along their tokens (a fixed cut for the sizes); the state
+ * then enters a part as the part before it left it, in fp32.
+ *   ws  gdn_selective_scan_workspace() bytes, 256-byte aligned (may be NULL if 0)
+ * ch any value; at most 2^30 tokens.  x, dt, Bm, Cm, z, y, A, h0 and ht 16-byte
+ * aligned, D and dt_bias 4-byte.
+ * gdn_selective_scan_varlen: the same on `seqs` packed sequences (x, dt, z, y
+ * [total_T, ch], Bm, Cm [total_T, N], states [seqs, ch, N]); cu_seqlens as in
+ * gdn_chunk_fwd_varlen (an empty sequence passes its state on; tokens that
+ * belong to no sequence are left alone).
+ * Errors: GDN_ERR_INVALID_ARG (null required pointers, sizes < 1, misalignment,
+ * an output that overlaps an input, another output or the workspace),
+ * GDN_ERR_UNSUPPORTED (N or types not listed, sizes beyond the limits),
+ * GDN_ERR_WORKSPACE, GDN_ERR_HIP.  Asynchronous on `stream`.
+ */
+size_t gdn_selective_scan_workspace(int B, int T, int ch, int N);
+gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                              const float *D, const void *z, const float *dt_bias, const float *h0, void *y, float *ht,
+                              int B, int T, int ch, int N, gdn_dtype dtype, void *ws, size_t ws_bytes, void *stream);
+size_t gdn_selective_scan_varlen_workspace(int seqs, int total_T, int ch, int N);
+gdn_status gdn_selective_scan_varlen(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                     const int *cu_seqlens, const float *D, const void *z, const float *dt_bias,
+                                     const float *h0, void *y, float *ht, int seqs, int total_T, int ch, int N,
+                                     gdn_dtype dtype, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * gdn_selective_step -- one decode token of gdn_selective_scan for each of B
+ * sequences: x, dt, z, y [B, ch], Bm, Cm [B, N], h_in, h_out [B, ch, N] fp32;
+ * h_out may be h_in itself (in place).  The others, alignment and errors as
+ * gdn_selective_scan; B * ch * N / 4 below 2^32.  No workspace.
+ */
+gdn_status gdn_selective_step(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
+                              const float *D, const void *z, const float *dt_bias, const float *h_in, float *h_out,
+                              void *y, int B, int ch, int N, gdn_dtype dtype, void *stream);
+
+/*
  * gdn_clock_probe -- measurement aid, not part of the operation: enqueues
  * nblocks single-wave workgroups that each spin for spin_us microseconds of
  * real time and write two counts to out (device, 2 * nblocks uint64): the

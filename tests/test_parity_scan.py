@@ -1,0 +1,355 @@
+"""GPU parity of the short convolution, the selective scan and its single-token
+step, through the public calls, against the fp64 definitions in oracle/scan.py.
+
+The convolution without activation runs on small whole numbers, which fp32
+holds exactly.  With SiLU: W + 1 fp32 roundings of the sum and the sigmoid
+within 2^-22 |v| + 2^-20: bar 1.1 (W + 1) 2^-24 sum|w x| + (2^-22 |v| + 2^-20) |y|.
+The scan's bars come with its definition (what fp32 steps may be off by, decaying
+as the state does); outputs in bf16 add 2^-8 of the value."""
+import numpy as np
+import pytest
+
+import gated_delta_rule_34_amd as gdn
+from oracle import scan as sc
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+HALF = {BF: 2.0 ** -8, F32: 0.0}
+
+
+def _t(rng, shape, dt, scale=1.0):
+    return torch.from_numpy((scale * rng.standard_normal(shape)).astype(np.float32)).to(dt).cuda()
+
+
+def _ints(rng, shape, top, dt):
+    return torch.from_numpy(rng.integers(-top, top + 1, shape).astype(np.float32)).to(dt).cuda()
+
+
+def _h(t):
+    return None if t is None else t.detach().float().cpu().double().numpy()
+
+
+def _close(x, ref, bar, what):
+    bad = np.abs(x - ref) - bar
+    assert np.isfinite(x).all() and bad.max() <= 0, f"{what}: worst excess {bad.max():.3e}"
+
+
+def _cu(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+# ---- the convolution ------------------------------------------------------------
+
+CONV = [(1, 1, 1, 4), (2, 1, 40, 3), (64, 1, 256, 4), (3, 2, 7, 2), (2, 3, 1031, 4), (1, 4, 64, 4), (1, 16, 8, 4),
+        (2, 17, 24, 3), (5, 33, 129, 4), (3, 300, 72, 4), (2, 1000, 2048, 2), (1, 5000, 256, 4)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("B,T,C,W", CONV)
+def test_conv_exact(B, T, C, W, dt):
+    rng = np.random.default_rng(B + T + C)
+    x, w, b = _ints(rng, (B, T, C), 3, dt), _ints(rng, (C, W), 3, F32), _ints(rng, (C,), 9, F32)
+    st = _ints(rng, (B, W - 1, C), 3, F32)
+    for bias, state in ((b, st), (None, None)):
+        ref, rs = sc.causal_conv(_h(x), _h(w), _h(bias), _h(state), "none")
+        y, new = gdn.gdn_causal_conv(x, w, bias=bias, act="none", conv_state=state)
+        assert y.dtype == dt
+        np.testing.assert_array_equal(_h(y), ref)      # whole numbers below 256: bf16 holds them
+        np.testing.assert_array_equal(_h(new), rs)
+    held = st.clone()
+    y, new = gdn.gdn_causal_conv(x, w, bias=b, act="none", conv_state=held, update_conv_state=True)
+    ref, rs = sc.causal_conv(_h(x), _h(w), _h(b), _h(st), "none")
+    assert new is held
+    np.testing.assert_array_equal(_h(y), ref)
+    np.testing.assert_array_equal(_h(new), rs)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("C,W", [(40, 4), (129, 3), (512, 2)])
+def test_conv_silu_and_bias(C, W, dt):
+    rng = np.random.default_rng(C)
+    x, w, b, st = _t(rng, (3, 50, C), dt), _t(rng, (C, W), F32), _t(rng, (C,), F32), _t(rng, (3, W - 1, C), F32)
+    ref, _ = sc.causal_conv(_h(x), _h(w), _h(b), _h(st))
+    v, _ = sc.causal_conv(_h(x), _h(w), _h(b), _h(st), "none")
+    mag, _ = sc.causal_conv(np.abs(_h(x)), np.abs(_h(w)), np.abs(_h(b)), np.abs(_h(st)), "none")
+    y, _ = gdn.gdn_causal_conv(x, w, bias=b, conv_state=st)
+    bar = 1.1 * (W + 1) * 2.0 ** -24 * mag + (2.0 ** -22 * np.abs(v) + 2.0 ** -20) * np.abs(ref)
+    _close(_h(y), ref, bar + HALF[dt] * (np.abs(ref) + bar), "y")
+
+
+@pytest.mark.parametrize("lens", [[5], [1, 1, 1], [0, 3, 0, 0, 1, 40, 0], [100, 2, 17, 0, 300], [1] * 70, [16, 16, 4, 12]])
+def test_conv_packed(lens):
+    rng = np.random.default_rng(len(lens))
+    C, W, T = 136, 4, sum(lens)
+    x, w, b = _ints(rng, (T + 5, C), 3, BF), _ints(rng, (C, W), 3, F32), _ints(rng, (C,), 9, F32)
+    for state in (None, _ints(rng, (len(lens), W - 1, C), 3, F32)):
+        out = torch.full_like(x, 7.0)
+        y, new = gdn.gdn_causal_conv_varlen(x, w, _cu(lens), bias=b, act="none", conv_state=state, out=out)
+        assert (y[T:] == 7).all()                      # tokens of no sequence
+        at = 0
+        for i, n in enumerate(lens):
+            s = None if state is None else _h(state[i:i + 1])
+            ref, rs = sc.causal_conv(_h(x[at:at + n])[None], _h(w), _h(b), s, "none")
+            np.testing.assert_array_equal(_h(y[at:at + n]), ref[0])
+            np.testing.assert_array_equal(_h(new[i]), rs[0])
+            at += n
+        if state is not None:
+            want = new.clone()
+            y2, new2 = gdn.gdn_causal_conv_varlen(x, w, _cu(lens), bias=b, act="none", conv_state=state,
+                                                  update_conv_state=True)
+            assert new2 is state and torch.equal(new2, want) and torch.equal(y2[:T], y[:T])
+
+
+# ---- the scan -------------------------------------------------------------------
+
+
+def _inputs(rng, lead, ch, N, dt, z=True, h0=0):
+    p = {"x": _t(rng, lead + (ch,), dt), "dt": _t(rng, lead + (ch,), dt), "B": _t(rng, lead + (N,), dt),
+         "C": _t(rng, lead + (N,), dt), "A": -torch.exp(_t(rng, (ch, N), F32)), "D": _t(rng, (ch,), F32),
+         "dt_bias": _t(rng, (ch,), F32) - 3.0, "z": _t(rng, lead + (ch,), dt, 2.0) if z else None}
+    p["h0"] = _t(rng, (h0, ch, N), F32) if h0 else None
+    return p
+
+
+def _reference(p, per_step=0.0):
+    return sc.selective_scan(*(_h(p[k]) for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0")), per_step=per_step)
+
+
+def _check(y, h, ref, dt, what=""):
+    ry, rh, by, bh = ref
+    _close(_h(y), ry, by + HALF[dt] * (np.abs(ry) + by), what + "y")
+    _close(_h(h), rh, bh, what + "h")
+
+
+# one token; part tiles; one segment (many groups of channels); a sequence in parts; odd channels; each state count
+SCAN = [(1, 1, 1, 8), (3, 1, 64, 16), (2, 5, 65, 32), (1, 16, 64, 64), (2, 17, 130, 16), (70, 40, 250, 8), (130, 20, 128, 16),
+        (1, 64, 64, 16), (1, 65, 64, 16), (1, 200, 70, 16), (2, 333, 129, 32), (1, 1000, 40, 8), (3, 150, 24, 64)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n,T,ch,N", SCAN)
+def test_scan(n, T, ch, N, dt):
+    rng = np.random.default_rng(n + T + ch)
+    p = _inputs(rng, (n, T), ch, N, dt, h0=n)
+    y, h = gdn.gdn_selective_scan(**p)
+    assert y.dtype == dt and h.dtype == F32
+    _check(y, h, _reference(p, T * 2.0 ** -24), dt)
+    again = gdn.gdn_selective_scan(**p)
+    assert torch.equal(again[0], y) and torch.equal(again[1], h)
+    held = dict(p, h0=p["h0"].clone())
+    y2, h2 = gdn.gdn_selective_scan(**held, final_state=held["h0"])
+    assert h2 is held["h0"] and torch.equal(h2, h) and torch.equal(y2, y)
+    y3, none = gdn.gdn_selective_scan(**p, output_final_state=False)
+    assert none is None and torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("n,T,ch", [(2, 100, 72), (1, 500, 64)])
+def test_scan_without_what_is_optional(n, T, ch):
+    rng = np.random.default_rng(n)
+    p = _inputs(rng, (n, T), ch, 16, F32, z=False)
+    p["dt"] = p["dt"] - 3.0
+    p.update(D=None, dt_bias=None)
+    y, h = gdn.gdn_selective_scan(**p)
+    _check(y, h, _reference(p, T * 2.0 ** -24), F32)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("lens", [[5], [1, 1, 1], [0, 3, 0, 0, 1, 40, 0], [100, 2, 17, 0, 300], [1] * 70, [64, 64, 128],
+                                  [700], [15, 0, 257, 1, 1, 60]])
+def test_scan_packed(lens, dt):
+    """Against each sequence's definition; behind the last sequence nothing changes; in place alike."""
+    rng = np.random.default_rng(sum(lens))
+    T, ch, N, k = sum(lens), 72, 16, len(lens)
+    for h0 in (0, k):
+        p = _inputs(rng, (T + 5,), ch, N, dt, h0=h0)
+        out = torch.full_like(p["x"], 7.0)
+        y, h = gdn.gdn_selective_scan_varlen(**p, cu_seqlens=_cu(lens), out=out)
+        assert (y[T:] == 7).all()
+        at = 0
+        for i, n in enumerate(lens):
+            if n == 0:
+                assert (h[i] == (p["h0"][i] if h0 else 0)).all()
+                continue
+            q = dict(p, **{s: p[s][None, at:at + n] for s in ("x", "dt", "B", "C", "z")})
+            q["h0"] = p["h0"][i:i + 1] if h0 else None
+            _check(y[None, at:at + n], h[i:i + 1], _reference(q, n * 2.0 ** -24), dt, f"sequence {i} ")
+            at += n
+        if h0:
+            held = dict(p, h0=p["h0"].clone())
+            y2, h2 = gdn.gdn_selective_scan_varlen(**held, cu_seqlens=_cu(lens), final_state=held["h0"])
+            assert torch.equal(h2, h) and torch.equal(y2[:T], y[:T])
+
+
+@pytest.mark.parametrize("cu", [[0, 400, 100, 600], [-50, 10, 2000], [300, 200, 100], [5, 5, 5], [7, 90, 600]])
+def test_malformed_offsets_stay_in_range(cu):
+    """They give wrong sequences, but write only to the outputs (guard rows around every one of them)."""
+    rng = np.random.default_rng(1)
+    T, ch, N = 600, 64, 16
+    p = _inputs(rng, (T,), ch, N, F32, h0=len(cu) - 1)
+    big, hbig = torch.full((T + 64, ch), 7.0, device="cuda"), torch.full((len(cu) + 1, ch, N), 7.0, device="cuda")
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    gdn.gdn_selective_scan_varlen(**p, cu_seqlens=c, out=big[32:T + 32], final_state=hbig[1:-1])
+    w, s = _t(rng, (ch, 4), F32), _t(rng, (len(cu) - 1, 3, ch), F32)
+    big2 = big.clone()
+    gdn.gdn_causal_conv_varlen(p["x"], w, c, conv_state=s, out=big2[32:T + 32])
+    gdn.gdn_causal_conv_varlen(p["x"], w, c, conv_state=s, update_conv_state=True)
+    torch.cuda.synchronize()
+    for b in (big, big2):
+        assert (b[:32] == 7).all() and (b[T + 32:] == 7).all()
+    assert (hbig[0] == 7).all() and (hbig[-1] == 7).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n,ch,N", [(1, 1, 8), (3, 65, 16), (64, 2048, 16), (5, 130, 32), (2, 77, 64)])
+def test_step(n, ch, N, dt):
+    rng = np.random.default_rng(n + ch)
+    p = _inputs(rng, (n,), ch, N, dt, h0=n)
+    h0 = p.pop("h0")
+    new = torch.empty_like(h0)
+    y, h = gdn.gdn_selective_step(**p, state=h0, state_out=new)
+    assert h is new
+    q = {k: v[:, None] if k in ("x", "dt", "B", "C", "z") else v for k, v in p.items()}
+    _check(y[:, None], h, _reference(dict(q, h0=h0)), dt)
+    held = h0.clone()
+    y2, h2 = gdn.gdn_selective_step(**p, state=held)
+    assert h2 is held and torch.equal(held, new) and torch.equal(y2, y)
+    p.update(z=None, D=None)
+    q.update(z=None, D=None)
+    y, h = gdn.gdn_selective_step(**p, state=h0, state_out=new)
+    _check(y[:, None], h, _reference(dict(q, h0=h0)), dt)
+
+
+def test_extreme_steps_and_decays():
+    """softplus from far below zero to far above; decays that underflow; A of zero."""
+    rng = np.random.default_rng(4)
+    p = _inputs(rng, (1, 100), 64, 16, F32, h0=1)
+    p["dt"] = torch.linspace(-60, 60, 100, device="cuda")[None, :, None].expand(1, 100, 64).contiguous()
+    p["dt_bias"] = torch.zeros(64, device="cuda")
+    p["A"][:, 3] = 0.0
+    p["A"][:, 4] = -1e30
+    y, h = gdn.gdn_selective_scan(**p)
+    _check(y, h, _reference(p, 100 * 2.0 ** -24), F32)
+
+
+def test_nan_stays_in_its_channel_and_sequence():
+    rng = np.random.default_rng(5)
+    p = _inputs(rng, (2, 90), 130, 16, F32)
+    want, hw = gdn.gdn_selective_scan(**p)
+    p["x"][1, 40, 70] = float("nan")
+    y, h = gdn.gdn_selective_scan(**p)
+    assert torch.isnan(y[1, 40:, 70]).all() and torch.isnan(h[1, 70]).all()
+    y[1, 40:, 70], h[1, 70] = want[1, 40:, 70], hw[1, 70]
+    assert torch.equal(y, want) and torch.equal(h, hw)
+
+
+def test_prompt_then_tokens_and_graph():
+    """A mixer as a model runs it: projection, convolution, projections of its output, scan, projection -- a prompt,
+    then tokens one by one, eagerly and in a captured graph replayed with eager work between, against the whole
+    sequence at once.  The convolution's outputs are bf16 in both, so they agree up to fp32 sums; the scans differ by
+    the order of fp32 steps only."""
+    rng = np.random.default_rng(7)
+    B, T, P, E, ch, N = 2, 90, 77, 64, 128, 16
+    w = {k: _t(rng, s, BF, s[1] ** -0.5) for k, s in (("x", (ch, E)), ("z", (ch, E)), ("dt", (ch, ch)), ("B", (N, ch)),
+                                                      ("C", (N, ch)), ("o", (E, ch)))}
+    cw, cb = _t(rng, (ch, 4), F32, 0.5), _t(rng, (ch,), F32, 0.1)
+    A, D, db = -torch.exp(_t(rng, (ch, N), F32)), _t(rng, (ch,), F32), _t(rng, (ch,), F32) - 3
+    nw, nb = torch.ones(E, device="cuda"), torch.zeros(E, device="cuda")
+    x = _t(rng, (B, T, E), BF)
+
+    def mixer(x, conv, h, token):
+        u = gdn.gdn_add_layernorm(x, nw, bias=nb)[0]
+        z = gdn.gdn_linear(u, w["z"])[0]
+        c, conv = gdn.gdn_causal_conv(gdn.gdn_linear(u, w["x"])[0], cw, bias=cb, conv_state=conv)
+        dt, Bm, Cm = (gdn.gdn_linear(c, w[k])[0] for k in ("dt", "B", "C"))
+        if token:
+            y, h = gdn.gdn_selective_step(c[:, 0], dt[:, 0].contiguous(), A, Bm[:, 0].contiguous(), Cm[:, 0].contiguous(),
+                                          h, D=D, z=z[:, 0].contiguous(), dt_bias=db, state_out=torch.empty_like(h))
+            y = y[:, None]
+        else:
+            y, h = gdn.gdn_selective_scan(c, dt, A, Bm, Cm, D=D, z=z, dt_bias=db, h0=h)
+        return gdn.gdn_linear(y, w["o"], residual=x)[0], conv, h
+
+    whole, wc, wh = mixer(x, None, None, False)
+    out, conv, h = mixer(x[:, :P].contiguous(), None, None, False)
+    outs = [out]
+    cs, hs = conv.clone(), h.clone()
+    xt = x[:, P:P + 1].clone()
+    for t in range(P, T):
+        out, conv, h = mixer(x[:, t:t + 1].contiguous(), conv, h, True)
+        outs.append(out)
+    got = torch.cat(outs, 1)
+    assert torch.equal(conv, wc)
+
+    def near(a, b, tol):
+        assert float((a.float() - b.float()).norm() / b.float().norm()) <= tol
+
+    # a handful of bf16 values may round the other way, each by a step of 2^-8 of itself
+    near(got, whole, 2.0 ** -9)
+    near(h, wh, 2.0 ** -9)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        mixer(xt, cs, hs, True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, c2, h2 = mixer(xt, cs, hs, True)
+    conv, h = cs.clone(), hs.clone()
+    for t in range(P, P + 6):
+        xt.copy_(x[:, t:t + 1])
+        graph.replay()
+        eo, conv, h = mixer(x[:, t:t + 1].contiguous(), conv, h, True)
+        torch.cuda.synchronize()
+        assert torch.equal(o, eo) and torch.equal(c2, conv) and torch.equal(h2, h)
+        cs.copy_(c2)
+        hs.copy_(h2)
+        torch.cuda.synchronize()
+
+
+def test_scan_captured_and_on_two_streams():
+    """A scan in parts (with its workspace) in a graph replayed on new inputs, and two at once on two streams."""
+    rng = np.random.default_rng(8)
+    p, q = (_inputs(rng, (1, 700), 64, 16, BF, h0=1) for _ in range(2))
+    want = [gdn.gdn_selective_scan(**t) for t in (p, q)]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for st, t in zip(streams, (p, q)):
+        with torch.cuda.stream(st):
+            got.append([gdn.gdn_selective_scan(**t) for _ in range(4)][-1])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = gdn.gdn_selective_scan(**p)
+    for _ in range(4):
+        p["x"].copy_(_t(rng, (1, 700, 64), BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        ey, eh = gdn.gdn_selective_scan(**p)
+        assert torch.equal(y, ey) and torch.equal(h, eh)
+        torch.cuda.synchronize()
+
+
+def test_the_binding_refuses():
+    rng = np.random.default_rng(9)
+    p = _inputs(rng, (2, 8), 24, 16, BF)
+    with pytest.raises(TypeError):
+        gdn.gdn_selective_scan(**dict(p, dt=p["dt"].float()))
+    with pytest.raises(ValueError):
+        gdn.gdn_selective_scan(**dict(p, B=p["B"][:, :7].contiguous()))
+    with pytest.raises(ValueError):
+        gdn.gdn_selective_scan(**dict(p, h0=torch.zeros(1, 24, 16, device="cuda")))
+    with pytest.raises(RuntimeError):
+        gdn.gdn_selective_scan(**dict(p, A=p["A"][:, :12].contiguous(), B=p["B"][..., :12].contiguous(),
+                                      C=p["C"][..., :12].contiguous()))
+    with pytest.raises(ValueError):
+        gdn.gdn_selective_scan(**dict(p, x=p["x"][..., ::2]))
+    with pytest.raises(ValueError):
+        gdn.gdn_causal_conv(p["x"], torch.zeros(24, 4, device="cuda"), act="relu")
+    with pytest.raises(RuntimeError):
+        gdn.gdn_causal_conv(p["x"], torch.zeros(24, 5, device="cuda"))
+    with pytest.raises(ValueError):
+        gdn.gdn_causal_conv(p["x"], torch.zeros(24, 4, device="cuda"), update_conv_state=True)
