@@ -7,6 +7,8 @@
 // The decay differs in every channel and state, so there is no matrix product
 // in it: a state costs one exponential, two products and two multiply-adds a
 // token, on the vector unit.
+#include <limits.h>
+
 #include "gdn_device.h"
 #include "gdn_launch.h"
 #include "gdn_row.h"
@@ -56,15 +58,16 @@ struct ConvArgs {
 
 // A thread owns eight channels over a run of tokens: the window slides through
 // its registers, every input is read once a run (and W - 1 before it again).
-// Four tokens' loads are in flight at a time.
-template <class ET, int W>
+// Four tokens' loads are in flight while the four before them are computed.
+template <class ET, int W, bool PACKED>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
     constexpr int AT = 4, H = W - 1;
     const long id = (long)blockIdx.x * 256 + threadIdx.x;
     const long u = id / a.octets;
     const int c = (int)(id - u * a.octets) * 8;
+    const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     int n, start, end, t0, t1;
-    if (a.cu) {
+    if constexpr (PACKED) {
         if (u >= a.runs) return;
         t0 = (int)u * a.run;
         t1 = min(t0 + a.run, a.total);
@@ -81,7 +84,6 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
                 if (seq_at(a.cu, k + 1, a.total) > seq_at(a.cu, k, a.total)) continue;
                 for (int j = 0; j < H; ++j) {
                     const long at = ((long)k * H + j) * a.C;
-                    const f32x8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     store8v(a.state_out + at, a.state_in ? load8v(a.state_in + at, c, a.C) : zero, c, a.C);
                 }
             }
@@ -96,14 +98,13 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
     }
     const ET *x = (const ET *)a.x;
     ET *y = (ET *)a.y;
-    float w[8][W];
-    f32x8 bias;
+    using Raw = typename RawOf<ET>::type;
+    Raw ahead[AT];
+    auto fetch = [&](int t) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        bias[e] = a.bias && c + e < a.C ? a.bias[c + e] : 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[e][j] = c + e < a.C ? a.w[(long)(c + e) * W + j] : 0.f;
-    }
+        for (int k = 0; k < AT; ++k) ahead[k] = load_raw(x + (long)min(t + k, t1 - 1) * a.C, c, a.C);
+    };
+    fetch(t0);
     f32x8 hist[H];  // the H inputs before t, oldest first
     auto enter = [&](int t) {
 #pragma unroll
@@ -111,39 +112,61 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
             const int p = t - H + j;
             if (p >= start) hist[j] = raw_f32(load_raw(x + (long)p * a.C, c, a.C));
             else if (a.state_in) hist[j] = load8v(a.state_in + ((long)n * H + (p - start + H)) * a.C, c, a.C);
-            else hist[j] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            else hist[j] = zero;
         }
     };
-    bool in = false;  // hist holds what comes before t
-    for (int t = t0; t < t1; t += AT) {
-        typename RawOf<ET>::type raw[AT];
+    if (!PACKED) enter(t0);
+    f32x8 w[W], bias = zero;
+    if (a.bias) bias = load8v(a.bias, c, a.C);
+    if (c + 8 <= a.C) {
+        float v[8 * W];
 #pragma unroll
-        for (int k = 0; k < AT; ++k) raw[k] = load_raw(x + (long)min(t + k, t1 - 1) * a.C, c, a.C);
+        for (int e = 0; e < 8 * W; e += 4) *(f32x4 *)&v[e] = *(const f32x4_a4 *)(a.w + (long)c * W + e);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][e] = v[e * W + j];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][e] = c + e < a.C ? a.w[(long)(c + e) * W + j] : 0.f;
+    }
+    bool in = !PACKED;  // hist holds what comes before t
+    for (int t = t0; t < t1; t += AT) {
+        Raw raw[AT];
+#pragma unroll
+        for (int k = 0; k < AT; ++k) raw[k] = ahead[k];
+        if (t + AT < t1) fetch(t + AT);
 #pragma unroll
         for (int k = 0; k < AT; ++k) {
             const int now = t + k;
             if (now >= t1) break;
-            if (a.cu && now >= end) {  // on to the sequence of this token
-                do {
-                    ++n;
-                    if (n >= a.seqs) return;  // behind the last one
-                    start = seq_at(a.cu, n, a.total);
-                    end = seq_at(a.cu, n + 1, a.total);
-                } while (end <= now);
-                in = false;
+            if constexpr (PACKED) {
+                if (now >= end) {  // on to the sequence of this token
+                    do {
+                        ++n;
+                        if (n >= a.seqs) return;  // behind the last one
+                        start = seq_at(a.cu, n, a.total);
+                        end = seq_at(a.cu, n + 1, a.total);
+                    } while (end <= now);
+                    in = false;
+                }
+                if (now < start) continue;
+                if (!in) enter(now);
+                in = true;
             }
-            if (now < start) continue;
-            if (!in) enter(now);
-            in = true;
             const f32x8 v = raw_f32(raw[k]);
-            f32x8 o;
+            f32x8 o = bias;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float s = bias[e];
+            for (int j = 0; j < H; ++j)
 #pragma unroll
-                for (int j = 0; j < H; ++j) s = fmaf(w[e][j], hist[j][e], s);
-                s = fmaf(w[e][H], v[e], s);
-                o[e] = a.silu ? silu_of(s) : s;
+                for (int e = 0; e < 8; ++e) o[e] = fmaf(w[j][e], hist[j][e], o[e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(w[H][e], v[e], o[e]);
+            if (a.silu) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = silu_of(o[e]);
             }
             store8v(y + (long)now * a.C, o, c, a.C);
 #pragma unroll
@@ -182,7 +205,9 @@ template <class ET, int W>
 static hipError_t conv_run(ConvArgs a, float *state_out, bool apart, hipStream_t st) {
     a.state_out = apart ? nullptr : state_out;
     const long threads = (long)(a.cu ? 1 : a.seqs) * a.runs * a.octets;
-    hipLaunchKernelGGL((conv_kernel<ET, W>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, a);
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    if (a.cu) hipLaunchKernelGGL((conv_kernel<ET, W, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((conv_kernel<ET, W, false>), grid, dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !apart || !state_out) return e;
     const long n = (long)a.seqs * a.octets;
@@ -216,17 +241,16 @@ hipError_t launch_causal_conv(const void *x, const float *w, const float *bias, 
 template <class ET> struct Four;
 template <> struct Four<uint16_t> {
     uint2 u;
-    __device__ __forceinline__ void load(const uint16_t *p, int c, int D) {
+    __device__ __forceinline__ void load(const uint16_t *p) {
         typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
-        if (c + 4 <= D) {
-            const v2 t = *(const v2 *)(p + c);
-            u = make_uint2(t[0], t[1]);
-        } else {
-            uint32_t t[4];
+        const v2 t = *(const v2 *)p;
+        u = make_uint2(t[0], t[1]);
+    }
+    __device__ __forceinline__ void load(const uint16_t *p, int c, int D) {  // one by one up to D
+        uint32_t t[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = c + e < D ? p[c + e] : 0;
-            u = make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
-        }
+        for (int e = 0; e < 4; ++e) t[e] = c + e < D ? p[e] : 0;
+        u = make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
     }
     __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
     __device__ __forceinline__ float operator[](int e) const {
@@ -235,7 +259,7 @@ template <> struct Four<uint16_t> {
     }
     static __device__ __forceinline__ void store(uint16_t *p, const f32x4 &v, int c, int D) {
         typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
-        if (c + 4 <= D) {
+        if (c <= D - 4) {
             *(v2 *)(p + c) = v2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
         } else {
 #pragma unroll
@@ -246,18 +270,15 @@ template <> struct Four<uint16_t> {
 };
 template <> struct Four<float> {
     f32x4 u;
-    __device__ __forceinline__ void load(const float *p, int c, int D) {
-        if (c + 4 <= D) {
-            u = *(const f32x4_a4 *)(p + c);
-        } else {
+    __device__ __forceinline__ void load(const float *p) { u = *(const f32x4_a4 *)p; }
+    __device__ __forceinline__ void load(const float *p, int c, int D) {  // one by one up to D
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = c + e < D ? p[c + e] : 0.f;
-        }
+        for (int e = 0; e < 4; ++e) u[e] = c + e < D ? p[e] : 0.f;
     }
     __device__ __forceinline__ void zero() { u = f32x4{0.f, 0.f, 0.f, 0.f}; }
     __device__ __forceinline__ float operator[](int e) const { return u[e]; }
     static __device__ __forceinline__ void store(float *p, const f32x4 &v, int c, int D) {
-        if (c + 4 <= D) {
+        if (c <= D - 4) {
             *(f32x4_a4 *)(p + c) = v;
         } else {
 #pragma unroll
@@ -266,6 +287,9 @@ template <> struct Four<float> {
         }
     }
 };
+
+__device__ __forceinline__ float value_of(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ float value_of(float v) { return v; }
 
 constexpr int kTT = 16;   // tokens a tile
 constexpr int kCH = 64;   // channels a workgroup
@@ -288,11 +312,12 @@ struct Tile {
 };
 
 // Tiles of a segment in order, none across a sequence's end.  Every wave of a
-// workgroup walks the same ones.
+// workgroup walks the same ones; all of it is uniform, kept in scalar registers.
+template <bool PACKED>
 struct Walk {
     int pos, n, start, end, stop;
     __device__ __forceinline__ void init(const ScanArgs &a, int seg, int lane) {
-        if (a.cu) {
+        if constexpr (PACKED) {
             pos = seg * a.L;
             stop = min(pos + a.L, a.total);
             n = 0;  // sequences that end at or before pos
@@ -311,22 +336,23 @@ struct Walk {
         }
     }
     __device__ __forceinline__ void bounds(const ScanArgs &a) {
-        if (n < a.seqs) {
-            start = __builtin_amdgcn_readfirstlane(seq_at(a.cu, n, a.total));
-            end = __builtin_amdgcn_readfirstlane(seq_at(a.cu, n + 1, a.total));
-        } else {
-            start = end = stop;
+        const int k = min(n, a.seqs - 1);
+        start = __builtin_amdgcn_readfirstlane(seq_at(a.cu, k, a.total));
+        end = __builtin_amdgcn_readfirstlane(seq_at(a.cu, k + 1, a.total));
+    }
+    // On to the first sequence that ends behind token at; false: there is none.
+    __device__ __forceinline__ bool reach(const ScanArgs &a, int at) {
+        while (n < a.seqs && at >= end) {
+            ++n;
+            bounds(a);
         }
+        return n < a.seqs;
     }
     // The tile at pos; moves on.
     __device__ __forceinline__ Tile next(const ScanArgs &a) {
         Tile r{0, 0, 0, false, false};
-        if (a.cu) {
-            while (pos >= end && n < a.seqs) {
-                ++n;
-                bounds(a);
-            }
-            if (n >= a.seqs) return r;
+        if constexpr (PACKED) {
+            if (!reach(a, pos)) return r;
             pos = max(pos, start);
         }
         if (pos >= stop) return r;
@@ -350,31 +376,28 @@ struct Walk {
 // segments that follow (E, F); with several segments a sequence's state enters
 // a segment as E of the last, plus exp(A F) times what entered that, and so on
 // back to the segment where the sequence starts.
-template <class ET, int N, bool CARRY>
+template <class ET, int N, bool PACKED, bool CARRY>
 __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
     constexpr int SPL = N / 4, PB = N / 8;
+    constexpr int G = SPL == 16 ? 1 : SPL == 8 ? 2 : 4;
     typedef float sv __attribute__((ext_vector_type(SPL)));
+    struct Token {
+        float2 d;
+        sv b, c;
+    };
     __shared__ __attribute__((aligned(16))) float2 dd[2][kTT][kCH];
     __shared__ __attribute__((aligned(16))) float bc[2][2][kTT][N];
     __shared__ __attribute__((aligned(16))) float part[CARRY ? 1 : 2][CARRY ? 1 : kTT][4][kCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int groups = (a.ch + kCH - 1) / kCH, seg = blockIdx.x / groups, c0 = (blockIdx.x % groups) * kCH;
-    Walk walk;
+    const bool whole = c0 + kCH <= a.ch;
+    Walk<PACKED> walk;
     walk.init(a, seg, lane);
     if constexpr (CARRY) {
         // needed only where the sequence of the last token goes on; from its start
-        if (a.cu) {
-            Walk end = walk;
-            end.pos = walk.stop - 1;
-            while (end.pos >= end.end && end.n < a.seqs) {
-                ++end.n;
-                end.bounds(a);
-            }
-            if (end.n >= a.seqs || end.end <= walk.stop) return;
-            walk.n = end.n;
-            walk.start = end.start;
-            walk.end = end.end;
-            walk.pos = max(walk.pos, end.start);
+        if constexpr (PACKED) {
+            if (!walk.reach(a, walk.stop - 1) || walk.end <= walk.stop) return;
+            walk.pos = max(walk.pos, walk.start);
         } else if (walk.stop == walk.end) {
             return;
         }
@@ -390,7 +413,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
         }
         float sum = 0.f;
         if (!CARRY) {
-            if (a.cu && a.ht) {  // sequences without tokens pass their state on
+            if (PACKED && a.ht) {  // sequences without tokens pass their state on
                 for (int k = seg * 64; k < a.seqs; k += gridDim.x / groups * 64) {
                     const bool none = k + lane < a.seqs &&
                                       seq_at(a.cu, k + lane + 1, a.total) <= seq_at(a.cu, k + lane, a.total);
@@ -405,7 +428,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
                 }
             }
             if (walk.pos > walk.start && walk.n < a.seqs) {  // the sequence comes from segments before
-                const int q0 = a.cu ? walk.start / a.L : walk.n * a.per_seq;
+                const int q0 = PACKED ? walk.start / a.L : walk.n * a.per_seq;
                 if (live)
                     for (int q = q0; q < seg; ++q) {
                         const sv e = *(const sv *)(a.E + ((long)q * a.ch + c) * N + n0);
@@ -425,25 +448,44 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
                 for (int s = 0; s < SPL; ++s) h[s] = 0.f;
                 if (a.h0 && live) h = *(const sv *)(a.h0 + ((long)tile.seq * a.ch + c) * N + n0);
             }
-            auto token = [&](int k) {
-                const float2 d = dd[buf][k][lane];
-                const sv b = *(const sv *)&bc[buf][0][k][n0];
-                if (CARRY) sum += d.x;
-                sv cv;
-                if (!CARRY) cv = *(const sv *)&bc[buf][1][k][n0];
+            auto fetch = [&](Token &o, int k) {
+                o.d = dd[buf][k][lane];
+                o.b = *(const sv *)&bc[buf][0][k][n0];
+                if (!CARRY) o.c = *(const sv *)&bc[buf][1][k][n0];
+            };
+            auto token = [&](const Token &o, int k) {
+                if (CARRY) sum += o.d.x;
                 float y = 0.f;
 #pragma unroll
                 for (int s = 0; s < SPL; ++s) {
-                    h[s] = fmaf(__builtin_amdgcn_exp2f(d.x * A[s]), h[s], d.y * b[s]);
-                    if (!CARRY) y = s ? fmaf(cv[s], h[s], y) : cv[s] * h[s];
+                    h[s] = fmaf(__builtin_amdgcn_exp2f(o.d.x * A[s]), h[s], o.d.y * o.b[s]);
+                    if (!CARRY) y = s ? fmaf(o.c[s], h[s], y) : o.c[s] * h[s];
                 }
                 if (!CARRY) part[buf][k][wave][lane] = y;
             };
             if (tile.len == kTT) {
+                // what G tokens need leaves LDS while the G before them are computed
+                Token g[2][G];
 #pragma unroll
-                for (int k = 0; k < kTT; ++k) token(k);
+                for (int k = 0; k < G; ++k) fetch(g[0][k], k);
+#pragma unroll
+                for (int k0 = 0; k0 < kTT; k0 += G) {
+                    const int now = k0 / G & 1;
+                    if (k0 + G < kTT) {
+#pragma unroll
+                        for (int k = 0; k < G; ++k) fetch(g[now ^ 1][k], k0 + G + k);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int k = 0; k < G; ++k) token(g[now][k], k0 + k);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             } else {
-                for (int k = 0; k < tile.len; ++k) token(k);
+                for (int k = 0; k < tile.len; ++k) {
+                    Token o;
+                    fetch(o, k);
+                    token(o, k);
+                }
             }
             if (!CARRY && tile.last && a.ht && live) *(sv *)(a.ht + ((long)tile.seq * a.ch + c) * N + n0) = h;
             __syncthreads();
@@ -465,9 +507,10 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
             bias[e] = a.dt_bias && c + e < a.ch ? a.dt_bias[c + e] : 0.f;
             skip[e] = a.D && c + e < a.ch ? a.D[c + e] : 0.f;
         }
+        typedef ET bv __attribute__((ext_vector_type(PB)));
         struct In {
             Four<ET> x, dt, z;
-            ET b[PB];
+            bv b;
             int t, len;
         };
         auto load = [&](In &in) {
@@ -478,14 +521,20 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
             in.dt.zero();
             in.z.zero();
             if (k < in.len) {
-                const long row = (long)(in.t + k) * a.ch;
-                in.x.load((const ET *)a.x + row, c, a.ch);
-                in.dt.load((const ET *)a.dt + row, c, a.ch);
-                if (!CARRY && a.z) in.z.load((const ET *)a.z + row, c, a.ch);
+                const long at = (long)(in.t + k) * a.ch + c;
+                if (whole) {
+                    in.x.load((const ET *)a.x + at);
+                    in.dt.load((const ET *)a.dt + at);
+                    if (!CARRY && a.z) in.z.load((const ET *)a.z + at);
+                } else {
+                    in.x.load((const ET *)a.x + at, c, a.ch);
+                    in.dt.load((const ET *)a.dt + at, c, a.ch);
+                    if (!CARRY && a.z) in.z.load((const ET *)a.z + at, c, a.ch);
+                }
             }
-            const ET *p = (const ET *)(side ? a.C : a.B) + (long)(in.t + bt) * N + bn;
 #pragma unroll
-            for (int e = 0; e < PB; ++e) in.b[e] = bt < in.len ? p[e] : (ET)0;
+            for (int e = 0; e < PB; ++e) in.b[e] = 0;
+            if (bt < in.len) in.b = *(const bv *)((const ET *)(side ? a.C : a.B) + (long)(in.t + bt) * N + bn);
         };
         auto stage = [&](const In &in, int buf) {
 #pragma unroll
@@ -494,7 +543,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
                 *(f32x4 *)&dd[buf][k][cc + e] = f32x4{d0, d0 * in.x[e], d1, d1 * in.x[e + 1]};
             }
 #pragma unroll
-            for (int e = 0; e < PB; ++e) bc[buf][side][bt][bn + e] = load_elem(&in.b[e]);
+            for (int e = 0; e < PB; ++e) bc[buf][side][bt][bn + e] = value_of(in.b[e]);
         };
         auto finish = [&](const In &in, int buf) {
             if (k >= in.len) return;
@@ -506,7 +555,9 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
                 v[e] = fmaf(skip[e], in.x[e], v[e]);
                 if (a.z) v[e] *= silu_of(in.z[e]);
             }
-            Four<ET>::store((ET *)a.y + (long)(in.t + k) * a.ch, v, c, a.ch);
+            ET *row = (ET *)a.y + (long)(in.t + k) * a.ch;
+            if (whole) Four<ET>::store(row, v, c, INT_MAX);
+            else Four<ET>::store(row, v, c, a.ch);
         };
         In before, now, after, far;
         now.len = 0;
@@ -567,11 +618,13 @@ template <class ET, int N>
 static hipError_t scan_run(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
     const dim3 grid((unsigned)((a.ch + kCH - 1) / kCH) * (unsigned)p.segs);
     if (p.per_seq > 1) {
-        hipLaunchKernelGGL((scan_kernel<ET, N, true>), grid, dim3(512), 0, st, a);
+        if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, true, true>), grid, dim3(512), 0, st, a);
+        else hipLaunchKernelGGL((scan_kernel<ET, N, false, true>), grid, dim3(512), 0, st, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((scan_kernel<ET, N, false>), grid, dim3(512), 0, st, a);
+    if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, true, false>), grid, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((scan_kernel<ET, N, false, false>), grid, dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
@@ -622,8 +675,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(const ET *x, const ET *d
     const f32x4 h = *(const f32x4 *)(h0 + u * N + q);
     const f32x4 A4 = *(const f32x4 *)(A + (long)c * N + q);
     Four<ET> bv, cv;
-    bv.load(B + b * N, q, N);
-    cv.load(C + b * N, q, N);
+    bv.load(B + b * N + q);
+    cv.load(C + b * N + q);
     const float xv = load_elem(x + u);
     const float d = softplus(load_elem(dt + u) + (dt_bias ? dt_bias[c] : 0.f));
     f32x4 o;
