@@ -938,7 +938,8 @@ gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bi
 // Sizes of a scan: 32-bit token numbers, a grid of fewer than 2^32 threads.
 static gdn_status scan_check(int seqs, int T, long long total, int ch, int N, bool packed) {
     if (seqs < 1 || T < 1 || ch < 1 || N < 1) return GDN_ERR_INVALID_ARG;
-    if ((N != 8 && N != 16 && N != 32 && N != 64) || total > (1 << 30) || ch > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    if ((N != 8 && N != 16 && N != 32 && N != 64) || total > (1 << 30) || ch < 4 || ch > (1 << 24))
+        return GDN_ERR_UNSUPPORTED;
     const gdn::ScanPlan p = gdn::scan_plan(seqs, T, (int)total, ch, N, packed);
     return (long long)p.segs * ((ch + 63) / 64) < (1LL << 23) ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }

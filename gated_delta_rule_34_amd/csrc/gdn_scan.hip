@@ -21,21 +21,18 @@ __device__ __forceinline__ float silu_of(float z) {
 }
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|).  log1p(e) = 2 atanh(s)
-// with s = e / (2 + e) <= 1/3, by its odd series to s^15 (the next term is
-// 2e-9): small steps keep their relative accuracy, which the logarithm of
-// 1 + e would lose.
+// with s = e / (2 + e) <= 1/3, atanh(s) = s P(s^2) with P of degree 4 fitted so
+// that the largest relative error is least (4e-9): small steps keep their
+// relative accuracy, which the logarithm of 1 + e would lose.
 __device__ __forceinline__ float softplus(float v) {
     const float e = __builtin_amdgcn_exp2f(-fabsf(v) * LOG2E);
     const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
+    float p = 0.14089167f;
+    p = fmaf(p, q, 0.139803f);
+    p = fmaf(p, q, 0.20012455f);
+    p = fmaf(p, q, 0.33333158f);
     p = fmaf(p, q, 1.f);
-    return (v > 0.f ? v : 0.f) + 2.f * s * p;
+    return fmaf(s + s, p, v > 0.f ? v : 0.f);
 }
 
 // Sequence offsets, clamped so that malformed ones stay in range.
@@ -246,13 +243,13 @@ template <> struct Four<uint16_t> {
         const v2 t = *(const v2 *)p;
         u = make_uint2(t[0], t[1]);
     }
-    __device__ __forceinline__ void load(const uint16_t *p, int c, int D) {  // one by one up to D
-        uint32_t t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = c + e < D ? p[e] : 0;
-        u = make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
+    // value e becomes value e + n (n < 4), zero past the last
+    __device__ __forceinline__ Four shifted(int n) const {
+        const uint64_t v = ((uint64_t)u.y << 32 | u.x) >> (16 * n);
+        Four o;
+        o.u = make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+        return o;
     }
-    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
     __device__ __forceinline__ float operator[](int e) const {
         const uint32_t v = e < 2 ? u.x : u.y;
         return __uint_as_float(e & 1 ? v & 0xffff0000u : v << 16);
@@ -271,11 +268,11 @@ template <> struct Four<uint16_t> {
 template <> struct Four<float> {
     f32x4 u;
     __device__ __forceinline__ void load(const float *p) { u = *(const f32x4_a4 *)p; }
-    __device__ __forceinline__ void load(const float *p, int c, int D) {  // one by one up to D
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = c + e < D ? p[e] : 0.f;
+    __device__ __forceinline__ Four shifted(int n) const {
+        Four o;
+        o.u = n == 0 ? u : n == 1 ? f32x4{u[1], u[2], u[3], 0.f} : n == 2 ? f32x4{u[2], u[3], 0.f, 0.f} : f32x4{u[3], 0.f, 0.f, 0.f};
+        return o;
     }
-    __device__ __forceinline__ void zero() { u = f32x4{0.f, 0.f, 0.f, 0.f}; }
     __device__ __forceinline__ float operator[](int e) const { return u[e]; }
     static __device__ __forceinline__ void store(float *p, const f32x4 &v, int c, int D) {
         if (c <= D - 4) {
@@ -369,15 +366,15 @@ struct Walk {
 // A workgroup owns 64 channels of a segment.  Four waves scan: a lane holds a
 // quarter of a channel's states, so that what a token costs them is its
 // arithmetic and four LDS accesses, and leaves its part of y in LDS.  Four
-// waves work beside them, a tile ahead and a tile behind: they load x, dt, z, B
-// and C (two tiles ahead), compute d and d x once per token and channel, and
-// turn the parts of y into outputs.  One barrier a tile.
+// waves work beside them: they compute d and d x once per token and channel a
+// tile ahead, and turn the parts of y into outputs a tile behind.  One barrier a
+// tile.
 // CARRY: only the state at the segment's end, and the sum of d, for the
 // segments that follow (E, F); with several segments a sequence's state enters
 // a segment as E of the last, plus exp(A F) times what entered that, and so on
 // back to the segment where the sequence starts.
 template <class ET, int N, bool PACKED, bool CARRY>
-__global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
+__global__ __launch_bounds__(512, N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) {
     constexpr int SPL = N / 4, PB = N / 8;
     constexpr int G = SPL == 16 ? 1 : SPL == 8 ? 2 : 4;
     typedef float sv __attribute__((ext_vector_type(SPL)));
@@ -429,16 +426,44 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
             }
             if (walk.pos > walk.start && walk.n < a.seqs) {  // the sequence comes from segments before
                 const int q0 = PACKED ? walk.start / a.L : walk.n * a.per_seq;
+                // four segments' values are asked for together: one after the other, their latencies would add up
+                constexpr int AT = 4;
                 if (live)
-                    for (int q = q0; q < seg; ++q) {
-                        const sv e = *(const sv *)(a.E + ((long)q * a.ch + c) * N + n0);
-                        const float f = a.F[(long)q * a.ch + c];
+                    for (int q = q0; q < seg; q += AT) {
+                        sv e[AT];
+                        float f[AT];
 #pragma unroll
-                        for (int s = 0; s < SPL; ++s)
-                            h[s] = q == q0 ? e[s] : fmaf(__builtin_amdgcn_exp2f(f * A[s]), h[s], e[s]);
+                        for (int i = 0; i < AT; ++i) {
+                            const long at = (long)min(q + i, seg - 1) * a.ch + c;
+                            e[i] = *(const sv *)(a.E + at * N + n0);
+                            f[i] = a.F[at];
+                        }
+#pragma unroll
+                        for (int i = 0; i < AT; ++i) {
+                            if (q + i >= seg) break;
+#pragma unroll
+                            for (int s = 0; s < SPL; ++s)
+                                h[s] = q + i == q0 ? e[i][s] : fmaf(__builtin_amdgcn_exp2f(f[i] * A[s]), h[s], e[i][s]);
+                        }
                     }
             }
         }
+        __builtin_amdgcn_s_setprio(3);  // the others fill the gaps these waves leave
+        auto fetch = [&](Token &o, int in, int k) {
+            o.d = dd[in][k][lane];
+            o.b = *(const sv *)&bc[in][0][k][n0];
+            if (!CARRY) o.c = *(const sv *)&bc[in][1][k][n0];
+        };
+        auto token = [&](const Token &o, int out, int k) {
+            if (CARRY) sum += o.d.x;
+            float y = 0.f;
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) {
+                h[s] = fmaf(__builtin_amdgcn_exp2f(o.d.x * A[s]), h[s], o.d.y * o.b[s]);
+                if (!CARRY) y = s ? fmaf(o.c[s], h[s], y) : o.c[s] * h[s];
+            }
+            if (!CARRY) part[out][k][wave][lane] = y;
+        };
         __syncthreads();
         for (int buf = 0;; buf ^= 1) {
             const Tile tile = walk.next(a);
@@ -448,55 +473,39 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
                 for (int s = 0; s < SPL; ++s) h[s] = 0.f;
                 if (a.h0 && live) h = *(const sv *)(a.h0 + ((long)tile.seq * a.ch + c) * N + n0);
             }
-            auto fetch = [&](Token &o, int k) {
-                o.d = dd[buf][k][lane];
-                o.b = *(const sv *)&bc[buf][0][k][n0];
-                if (!CARRY) o.c = *(const sv *)&bc[buf][1][k][n0];
-            };
-            auto token = [&](const Token &o, int k) {
-                if (CARRY) sum += o.d.x;
-                float y = 0.f;
-#pragma unroll
-                for (int s = 0; s < SPL; ++s) {
-                    h[s] = fmaf(__builtin_amdgcn_exp2f(o.d.x * A[s]), h[s], o.d.y * o.b[s]);
-                    if (!CARRY) y = s ? fmaf(o.c[s], h[s], y) : o.c[s] * h[s];
-                }
-                if (!CARRY) part[buf][k][wave][lane] = y;
-            };
             if (tile.len == kTT) {
                 // what G tokens need leaves LDS while the G before them are computed
                 Token g[2][G];
 #pragma unroll
-                for (int k = 0; k < G; ++k) fetch(g[0][k], k);
+                for (int k = 0; k < G; ++k) fetch(g[0][k], buf, k);
 #pragma unroll
                 for (int k0 = 0; k0 < kTT; k0 += G) {
                     const int now = k0 / G & 1;
                     if (k0 + G < kTT) {
 #pragma unroll
-                        for (int k = 0; k < G; ++k) fetch(g[now ^ 1][k], k0 + G + k);
+                        for (int k = 0; k < G; ++k) fetch(g[now ^ 1][k], buf, k0 + G + k);
                     }
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int k = 0; k < G; ++k) token(g[now][k], k0 + k);
+                    for (int k = 0; k < G; ++k) token(g[now][k], buf, k0 + k);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
                 for (int k = 0; k < tile.len; ++k) {
                     Token o;
-                    fetch(o, k);
-                    token(o, k);
+                    fetch(o, buf, k);
+                    token(o, buf, k);
                 }
             }
             if (!CARRY && tile.last && a.ht && live) *(sv *)(a.ht + ((long)tile.seq * a.ch + c) * N + n0) = h;
             __syncthreads();
         }
+        __syncthreads();  // the turn in which the others finish the last tile
         if constexpr (CARRY) {
             if (live) {
                 *(sv *)(a.E + ((long)seg * a.ch + c) * N + n0) = h;
                 if (wave == 0) a.F[(long)seg * a.ch + c] = sum;
             }
-        } else {
-            __syncthreads();
         }
     } else {
         const int id = threadIdx.x - 256, k = id >> 4, cc = (id & 15) * 4, c = c0 + cc;
@@ -513,30 +522,30 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
             bv b;
             int t, len;
         };
+        // Loads are issued for every thread and every tile, so that the wait
+        // for one is not a wait for all: a thread whose token or channels the
+        // tile lacks reads what another one does (its values are not used).
+        // Channels past the last are reached by a shift.
+        const int cl = min(c, a.ch - 4), shift = min(c - cl, 3);
+        const void *const zp = a.z ? a.z : a.x;
+        const char *const bp = (const char *)(side ? a.C : a.B);
         auto load = [&](In &in) {
             const Tile tile = walk.next(a);
             in.t = tile.t;
             in.len = tile.len;
-            in.x.zero();
-            in.dt.zero();
-            in.z.zero();
-            if (k < in.len) {
-                const long at = (long)(in.t + k) * a.ch + c;
-                if (whole) {
-                    in.x.load((const ET *)a.x + at);
-                    in.dt.load((const ET *)a.dt + at);
-                    if (!CARRY && a.z) in.z.load((const ET *)a.z + at);
-                } else {
-                    in.x.load((const ET *)a.x + at, c, a.ch);
-                    in.dt.load((const ET *)a.dt + at, c, a.ch);
-                    if (!CARRY && a.z) in.z.load((const ET *)a.z + at, c, a.ch);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < PB; ++e) in.b[e] = 0;
-            if (bt < in.len) in.b = *(const bv *)((const ET *)(side ? a.C : a.B) + (long)(in.t + bt) * N + bn);
+            const int row = min(k, max(tile.len - 1, 0)), brow = min(bt, max(tile.len - 1, 0));
+            const long first = (long)tile.t * a.ch * (long)sizeof(ET);
+            const uint32_t at = ((uint32_t)row * (uint32_t)a.ch + (uint32_t)cl) * (uint32_t)sizeof(ET);
+            in.x.load((const ET *)((const char *)a.x + first + at));
+            in.dt.load((const ET *)((const char *)a.dt + first + at));
+            if (!CARRY) in.z.load((const ET *)((const char *)zp + first + at));
+            in.b = *(const bv *)(bp + (long)tile.t * (N * (long)sizeof(ET)) + ((uint32_t)brow * N + bn) * (uint32_t)sizeof(ET));
         };
-        auto stage = [&](const In &in, int buf) {
+        auto stage = [&](In in, int buf) {
+            if (!whole) {
+                in.x = in.x.shifted(shift);
+                in.dt = in.dt.shifted(shift);
+            }
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
                 const float d0 = softplus(in.dt[e] + bias[e]), d1 = softplus(in.dt[e + 1] + bias[e + 1]);
@@ -545,43 +554,47 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a) {
 #pragma unroll
             for (int e = 0; e < PB; ++e) bc[buf][side][bt][bn + e] = value_of(in.b[e]);
         };
-        auto finish = [&](const In &in, int buf) {
-            if (k >= in.len) return;
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) v += *(const f32x4 *)&part[buf][k][w][cc];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = fmaf(skip[e], in.x[e], v[e]);
-                if (a.z) v[e] *= silu_of(in.z[e]);
+        auto finish = [&](In in, int buf) {
+            if (!whole) {
+                in.x = in.x.shifted(shift);
+                in.z = in.z.shifted(shift);
             }
-            ET *row = (ET *)a.y + (long)(in.t + k) * a.ch;
-            if (whole) Four<ET>::store(row, v, c, INT_MAX);
-            else Four<ET>::store(row, v, c, a.ch);
+            f32x4 v = *(const f32x4 *)&part[buf][k][0][cc];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) v += *(const f32x4 *)&part[buf][k][w][cc];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(skip[e], in.x[e], v[e]);
+            if (a.z) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= silu_of(in.z[e]);
+            }
+            if (k < in.len) {
+                ET *row = (ET *)a.y + (long)(in.t + k) * a.ch;
+                if (whole) Four<ET>::store(row, v, c, INT_MAX);
+                else Four<ET>::store(row, v, c, a.ch);
+            }
         };
-        In before, now, after, far;
-        now.len = 0;
-        load(after);
-        load(far);
-        stage(after, 0);
-        __syncthreads();
-        for (int buf = 0;; buf ^= 1) {
-            before = now;
-            now = after;
-            after = far;
-            if (now.len == 0) {
-                if constexpr (!CARRY) {
-                    if (before.len) finish(before, buf ^ 1);
-                    __syncthreads();
-                }
-                break;
-            }
+        // Turn j, on which the others scan tile j: tile j + 2 is asked for,
+        // tile j - 1 finished and tile j + 1 staged.  The turn after the last
+        // tile's is one like the others, so that the sets in flight stay where
+        // they are.
+        In i0, i1, i2, i3{};
+        load(i0);
+        load(i1);
+        stage(i0, 0);
+        auto turn = [&](const In &before, const In &now, const In &after, In &far, int buf) {
             load(far);
-            if constexpr (!CARRY) {
-                if (before.len) finish(before, buf ^ 1);
-            }
-            if (after.len) stage(after, buf ^ 1);
+            if (!CARRY) finish(before, buf ^ 1);
+            stage(after, buf ^ 1);
             __syncthreads();
+            return now.len != 0;
+        };
+        __syncthreads();
+        for (;;) {
+            if (!turn(i3, i0, i1, i2, 0)) break;
+            if (!turn(i0, i1, i2, i3, 1)) break;
+            if (!turn(i1, i2, i3, i0, 0)) break;
+            if (!turn(i2, i3, i0, i1, 1)) break;
         }
     }
 }

@@ -62,6 +62,7 @@ def test_scan_rejects_bad_arguments(packed):
     for k in ("x", "dt", "A", "B", "C", "y") + (("cu",) if packed else ()):
         assert f(**{k: None}) == 1
     assert f(n=0) == 1 and f(T=0) == 1 and f(ch=0) == 1 and f(N=0) == 1
+    assert f(ch=3) == 2 and f(ch=(1 << 24) + 1) == 2
     assert f(N=12) == 2 and f(N=128) == 2 and f(dtype=F8) == 2 and f(T=(1 << 30) + 1) == 2
     for k in ("x", "dt", "A", "B", "C", "z", "h0", "y", "ht"):
         assert f(**{k: base[k] + 8}) == 1

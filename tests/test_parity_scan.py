@@ -124,7 +124,7 @@ def _check(y, h, ref, dt, what=""):
 
 
 # one token; part tiles; one segment (many groups of channels); a sequence in parts; odd channels; each state count
-SCAN = [(1, 1, 1, 8), (3, 1, 64, 16), (2, 5, 65, 32), (1, 16, 64, 64), (2, 17, 130, 16), (70, 40, 250, 8), (130, 20, 128, 16),
+SCAN = [(1, 1, 4, 8), (1, 3, 5, 16), (1, 100, 6, 8), (2, 40, 7, 16), (3, 1, 64, 16), (2, 5, 65, 32), (1, 16, 64, 64), (2, 17, 130, 16), (70, 40, 250, 8), (130, 20, 128, 16),
         (1, 64, 64, 16), (1, 65, 64, 16), (1, 200, 70, 16), (2, 333, 129, 32), (1, 1000, 40, 8), (3, 150, 24, 64)]
 
 
