@@ -603,14 +603,20 @@ __global__ __launch_bounds__(256) void scan_copy_kernel(const float *src, float 
     for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) dst[i] = src[i];
 }
 
-// How a scan is cut along its tokens: enough segments to give each compute
-// unit work.
+// How a scan is cut along its tokens.  In one part a workgroup takes T tokens at
+// the pace of one alone in its compute unit; in parts their work is divided by
+// the compute units, two workgroups in each, but every token is scanned twice
+// (the states between the parts).  4096 tokens, 16 states, 2048 channels: 4
+// sequences (128 groups of channels) 231 us in four parts, 302 in one; 5 (160)
+// 334 in four parts, which are more than two workgroups to a compute unit, and
+// 302 in one; 7 (224) 392 and 304.  Twice or half as many parts: 8192 tokens
+// of 2048 channels 128 and 142 us for 123.
 ScanPlan scan_plan(int seqs, int T, int total, int ch, int N, bool packed) {
     const long groups = (ch + kCH - 1) / kCH;
     ScanPlan p{};
     const long base = packed ? groups : groups * seqs;
     const long len = packed ? total : T;
-    long k = base >= 256 ? 1 : (512 + base - 1) / base;
+    long k = base > 128 ? 1 : 512 / base;
     const long most = (len + 63) / 64;
     if (k > most) k = most;
     long L = (len + k - 1) / k;
