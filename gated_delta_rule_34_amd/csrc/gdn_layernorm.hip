@@ -11,7 +11,9 @@
 // variance is taken of the differences to the mean, in a second turn over the
 // registers that hold the row: the difference of the two moments would lose
 // all bits where the mean is large beside the spread.  Bound by HBM: a row is
-// read once, held in registers while its sums are formed, and written once.
+// read once, held in registers while its sums are formed, and written once:
+// 32768 x 1024 from bf16 and a fp32 residual stream to e4m3 72 us, 5.1 TB/s (a
+// large copy reaches 5.15); 4096 x 4096 in bf16 25 us; 4 x 1024 3.2 us.
 // Rows are laid over threads as in the RMS norm: one wave up to 2048 columns
 // in the forward and 1024 in the backward, beyond that 256, 512 or 1024
 // threads with one LDS exchange per sum; columns in pieces of eight per
@@ -23,6 +25,25 @@
 
 namespace gdn {
 
+// Two sums over the TPR threads of a row in one exchange; sh holds TPR / 64
+// pairs and is written once per call.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2 *sh) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) {
+            a += sh[i].x;
+            b += sh[i].y;
+        }
+    }
+    return make_float2(a, b);
+}
+
 template <class XT, class RT, class OT, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, const RT *res, const float *w,
                                                                    const float *b, OT *y, RT *rout, float *mean,
@@ -30,7 +51,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
                                                                    float eps) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
     constexpr bool F8 = sizeof(OT) == 1;
-    __shared__ float sh[3][TPR / 64 + 1];
+    __shared__ float sh[2][TPR / 64 + 1];
+    __shared__ float2 sh2[TPR / 64 + 1];
     const int tid = threadIdx.x % TPR;
     const long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
     if (row >= rows) return;  // whole waves leave, and only where a row is one wave
@@ -56,8 +78,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += u[i][e];
+    // The mean's own rounding moves every difference alike: their sum says by
+    // how much, and takes it out of the variance and of the differences.
     const float m = row_sum<TPR>(sum, sh[0]) / (float)D;
-    float ss = 0.f;
+    float ss = 0.f, sd = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int left = D - (tid + i * TPR) * 8;  // columns of this piece and after it
@@ -65,12 +89,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
         for (int e = 0; e < 8; ++e) {
             u[i][e] = e < left ? u[i][e] - m : 0.f;
             ss = fmaf(u[i][e], u[i][e], ss);
+            sd += u[i][e];
         }
     }
-    ss = row_sum<TPR>(ss, sh[1]);
-    const float s = 1.f / sqrtf(ss / (float)D + eps);
+    const float2 both = row_sum2<TPR>(ss, sd, sh2);
+    const float off = both.y / (float)D;
+    const float var = fmaf(-off, off, both.x / (float)D);
+    const float s = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);  // NaN stays
     if (tid == 0) {
-        if (mean) mean[row] = m;
+        if (mean) mean[row] = m + off;
         if (rstd) rstd[row] = s;
     }
 #pragma unroll
@@ -80,7 +107,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
         if (b) load_piece(bv, b, (tid + i * TPR) * 8, D);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            u[i][e] *= s;
+            u[i][e] = (u[i][e] - off) * s;
             u[i][e] = b ? fmaf(u[i][e], wv[e], bv[e]) : u[i][e] * wv[e];
         }
     }
@@ -92,8 +119,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) am = max(am, __float_as_uint(u[i][e]) & 0x7fffffffu);
-        am = row_max<TPR>(am, (uint32_t *)sh[2]);
-        float scale = __uint_as_float(am) * (1.f / 448.f);
+        am = row_max<TPR>(am, (uint32_t *)sh[1]);
+        float scale = __uint_as_float(am) / 448.f;
         if (scale == 0.f) scale = 1.f;
         if (tid == 0) yscale[row] = scale;
         const QuantRow q(scale);
@@ -105,31 +132,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
     }
 }
 
-// Two sums over the TPR threads of a row in one exchange; sh holds TPR / 64
-// pairs and is written once per call.
-template <int TPR>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2 *sh) {
-    a = wave_sum(a);
-    b = wave_sum(b);
-    if constexpr (TPR > 64) {
-        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_float2(a, b);
-        __syncthreads();
-        a = b = 0.f;
-#pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) {
-            a += sh[i].x;
-            b += sh[i].y;
-        }
-    }
-    return make_float2(a, b);
-}
-
 // Backward.  A workgroup walks rows (its first row, then every RPB * grid rows
 // on) and keeps the column sums of dy xhat and dy in registers; they leave as
 // one row of 2 D partial sums per workgroup, which ln_colsum_kernel adds up in
 // a fixed order (no atomics, so results repeat bit for bit).  The next row's
 // loads are issued before this row's sums where the registers hold both
-// (AHEAD).
+// (AHEAD).  32768 x 1024 in bf16 with dr 51 us, 5.2 TB/s of dy, r, dr and dx;
+// 16384 x 5120 in fp32 197 us, 5.1; beyond 8192 columns the two sums a column
+// crowd the registers: 4096 x 16384 in bf16 100 us, 4.0.
 template <class DT, class RT, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT *dy, const RT *r, const float *w,
                                                                        const float *mean, const float *rstd,
@@ -304,8 +314,18 @@ hipError_t launch_add_layernorm(const void *x, const void *res, const float *w, 
     return hipErrorInvalidValue;
 }
 
-// Workgroups of the backward, as measured for the RMS norm's.
-int ln_bwd_blocks(long rows, int D) { return norm_bwd_blocks(rows, D); }
+// Workgroups of the backward: enough to fill the card, few enough that their
+// partial sums (8 bytes a column and workgroup, written and read) stay small
+// beside the rows.  Measured at 128 to 1024 of them: 32768 x 256 in bf16 1024
+// best (30 us, 768 32, 512 42), 32768 x 1024 768 (51 us, 384 58, 1024 62),
+// 16384 x 5120 in fp32 512 (197 us, 256 244, 768 228), 4096 x 4096 in bf16 512
+// (33 us, 1024 42), 4096 x 8192 256 (45 us, 128 62, 512 53), 4096 x 16384 256
+// (100 us, 512 112).
+int ln_bwd_blocks(long rows, int D) {
+    const long groups = D <= 1024 ? (rows + 3) / 4 : rows;
+    const long most = D <= 512 ? 1024 : D <= 2048 ? 768 : D <= 6144 ? 512 : 256;
+    return (int)(groups < most ? groups : most);
+}
 
 template <class DT, class RT>
 static hipError_t launch_ln_bwd_t(const void *dy, const void *r, const float *w, const float *mean, const float *rstd,

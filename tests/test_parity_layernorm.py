@@ -105,6 +105,20 @@ def test_a_large_mean_leaves_the_spread():
     _close(_h(y), ref, 2.0 ** -17 * np.abs(ref) + 2.0 ** -23 * mean * rstd, "y")
 
 
+def test_the_mean_is_kept_beyond_its_rounding():
+    """Rows whose mean fp32 rounds (values around 1e4 + 1/3): the differences' own sum takes the rounding out again, so
+    y is as near as the differences themselves allow, 2^-24 of the values' size each."""
+    rng = np.random.default_rng(12)
+    x = _t(rng, (7, 4099), F32, 1.0) + 10000.0 + 1.0 / 3.0
+    y, _, m, s, _ = gdn.gdn_add_layernorm(x, torch.ones(4099, device="cuda"), return_stats=True)
+    ref, _, mean, rstd = ob.add_layernorm(_h(x), np.ones(4099))
+    _close(_h(m), mean, 2.0 ** -23 * mean, "mean")
+    _close(_h(s), rstd, 2.0 ** -17 * rstd, "rstd")
+    # x - m is exact here (both within a factor of two, multiples of 2^-10); off by at most 2^-18 of itself after the
+    # correction, whose sum has the error of 4099 additions of differences
+    _close(_h(y), ref, 2.0 ** -16 * np.maximum(np.abs(ref), 1.0), "y")
+
+
 def test_special_rows_stay_in_their_row():
     """Rows of one value, with an infinity and with a NaN: the others are as without them."""
     rng = np.random.default_rng(8)
