@@ -56,6 +56,8 @@ struct ConvArgs {
 // A thread owns eight channels over a run of tokens: the window slides through
 // its registers, every input is read once a run (and W - 1 before it again).
 // Four tokens' loads are in flight while the four before them are computed.
+// Bound by HBM: 8 x 4096 x 2048 channels in bf16 55 us, 4.8 TB/s (110 with each
+// four awaited first); one token of 64 sequences 4 us in a graph.
 template <class ET, int W, bool PACKED>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs a) {
     constexpr int AT = 4, H = W - 1;
@@ -363,19 +365,28 @@ struct Walk {
     }
 };
 
-// A workgroup owns 64 channels of a segment.  Four waves scan: a lane holds a
-// quarter of a channel's states, so that what a token costs them is its
-// arithmetic and four LDS accesses, and leaves its part of y in LDS.  Four
-// waves work beside them: they compute d and d x once per token and channel a
-// tile ahead, and turn the parts of y into outputs a tile behind.  One barrier a
-// tile.
+// A workgroup owns 64 channels of a segment.  SW waves scan: a lane holds N / SW
+// of a channel's states, so that what a token costs them is its arithmetic and
+// four LDS accesses, and leaves its part of y in LDS.  Four waves work beside
+// them: they compute d and d x once per token and channel a tile ahead, and turn
+// the parts of y into outputs a tile behind.  One barrier a tile.
+// Bound by the vector unit: a state costs a token four instructions and an
+// exponential (4.2 and 8.4 clocks each, measured), the rest of a channel and
+// token 125 / 16 instructions and one exponential and one reciprocal, twice.
+// 8 x 4096 x 2048 channels, 16 states, bf16 with skip and gate: that is 250 us,
+// and takes 302 with 256 workgroups, whose two waves a SIMD leave gaps (vector
+// unit busy 85 %; a single wave issues one instruction in 5.6 clocks), 255 with
+// two workgroups to a compute unit (16 x 2048 tokens).  HBM would take 105 us.
+// Tried and not kept: the 4x4x1 matrix products for B (d x) and for y (362 us;
+// for the first alone 310, and 250 with two workgroups), decays computed a
+// group of tokens ahead (310), staging two tiles ahead (313).
 // CARRY: only the state at the segment's end, and the sum of d, for the
 // segments that follow (E, F); with several segments a sequence's state enters
 // a segment as E of the last, plus exp(A F) times what entered that, and so on
 // back to the segment where the sequence starts.
-template <class ET, int N, bool PACKED, bool CARRY>
-__global__ __launch_bounds__(512, N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) {
-    constexpr int SPL = N / 4, PB = N / 8;
+template <class ET, int N, int SW, bool PACKED, bool CARRY>
+__global__ __launch_bounds__((SW + 4) * 64, SW == 8 ? 3 : N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) {
+    constexpr int SPL = N / SW, PB = N / 8;
     constexpr int G = SPL == 16 ? 1 : SPL == 8 ? 2 : 4;
     typedef float sv __attribute__((ext_vector_type(SPL)));
     struct Token {
@@ -384,7 +395,7 @@ __global__ __launch_bounds__(512, N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) 
     };
     __shared__ __attribute__((aligned(16))) float2 dd[2][kTT][kCH];
     __shared__ __attribute__((aligned(16))) float bc[2][2][kTT][N];
-    __shared__ __attribute__((aligned(16))) float part[CARRY ? 1 : 2][CARRY ? 1 : kTT][4][kCH];
+    __shared__ __attribute__((aligned(16))) float part[CARRY ? 1 : 2][CARRY ? 1 : kTT][SW][kCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int groups = (a.ch + kCH - 1) / kCH, seg = blockIdx.x / groups, c0 = (blockIdx.x % groups) * kCH;
     const bool whole = c0 + kCH <= a.ch;
@@ -399,7 +410,7 @@ __global__ __launch_bounds__(512, N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) 
             return;
         }
     }
-    if (wave < 4) {
+    if (wave < SW) {
         const int c = c0 + lane, n0 = wave * SPL;
         const bool live = c < a.ch;
         sv A, h;
@@ -508,7 +519,7 @@ __global__ __launch_bounds__(512, N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) 
             }
         }
     } else {
-        const int id = threadIdx.x - 256, k = id >> 4, cc = (id & 15) * 4, c = c0 + cc;
+        const int id = threadIdx.x - SW * 64, k = id >> 4, cc = (id & 15) * 4, c = c0 + cc;
         const int side = id >> 7, bt = (id & 127) * PB / N, bn = (id & 127) * PB % N;
         f32x4 bias, skip;
 #pragma unroll
@@ -561,7 +572,7 @@ __global__ __launch_bounds__(512, N == 64 ? 2 : 4) void scan_kernel(ScanArgs a) 
             }
             f32x4 v = *(const f32x4 *)&part[buf][k][0][cc];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) v += *(const f32x4 *)&part[buf][k][w][cc];
+            for (int w = 1; w < SW; ++w) v += *(const f32x4 *)&part[buf][k][w][cc];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = fmaf(skip[e], in.x[e], v[e]);
             if (a.z) {
@@ -637,13 +648,25 @@ template <class ET, int N>
 static hipError_t scan_run(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
     const dim3 grid((unsigned)((a.ch + kCH - 1) / kCH) * (unsigned)p.segs);
     if (p.per_seq > 1) {
-        if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, true, true>), grid, dim3(512), 0, st, a);
-        else hipLaunchKernelGGL((scan_kernel<ET, N, false, true>), grid, dim3(512), 0, st, a);
+        if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, 4, true, true>), grid, dim3(512), 0, st, a);
+        else hipLaunchKernelGGL((scan_kernel<ET, N, 4, false, true>), grid, dim3(512), 0, st, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, true, false>), grid, dim3(512), 0, st, a);
-    else hipLaunchKernelGGL((scan_kernel<ET, N, false, false>), grid, dim3(512), 0, st, a);
+    if constexpr (N >= 32) {
+        // one workgroup to a compute unit: eight scanning waves, so that each
+        // SIMD has three waves to choose from (8 x 2048 x 2048 channels with 32
+        // states 236 us against 269 with four, 8 x 1024 x 2048 with 64 205
+        // against 230; with 16, two to a lane, the reads from LDS outweigh it:
+        // 8 x 4096 x 2048 358 against 302)
+        if (grid.x <= 256) {
+            if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, 8, true, false>), grid, dim3(768), 0, st, a);
+            else hipLaunchKernelGGL((scan_kernel<ET, N, 8, false, false>), grid, dim3(768), 0, st, a);
+            return hipGetLastError();
+        }
+    }
+    if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, 4, true, false>), grid, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((scan_kernel<ET, N, 4, false, false>), grid, dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
@@ -678,7 +701,8 @@ hipError_t launch_selective_scan(const ScanPlan &p, const void *x, const void *d
 // ---- one token --------------------------------------------------------------------
 
 // A lane holds four states of a channel (16 bytes in, 16 out), N / 4 lanes a
-// channel; y is summed over them on DPP.  Bound by the states' traffic.
+// channel; y is summed over them on DPP.  Bound by the states' traffic: 256 x
+// 2048 channels with 16 states 15 us, 4.75 TB/s; 64 sequences 4.8 us in a graph.
 template <class ET, int N>
 __global__ __launch_bounds__(256) void scan_step_kernel(const ET *x, const ET *dt, const float *A, const ET *B,
                                                         const ET *C, const float *D, const ET *z,
