@@ -319,12 +319,15 @@ struct Walk {
         if constexpr (PACKED) {
             pos = seg * a.L;
             stop = min(pos + a.L, a.total);
-            n = 0;  // sequences that end at or before pos
-            for (int k = 0; k < a.seqs; k += 64) {
-                const bool before = k + lane < a.seqs && seq_at(a.cu, k + lane + 1, a.total) <= pos;
-                n += __popcll(__ballot(before));
+            // sequences that end at or before pos, 64 offsets a look
+            int lo = 0, hi = a.seqs;
+            while (lo < hi) {
+                const int step = (hi - lo + 63) / 64, k = lo + lane * step;
+                const int ended = __popcll(__ballot(k < hi && seq_at(a.cu, k + 1, a.total) <= pos));
+                hi = min(lo + ended * step, hi);
+                lo = ended ? lo + (ended - 1) * step + 1 : lo;
             }
-            n = __builtin_amdgcn_readfirstlane(n);
+            n = __builtin_amdgcn_readfirstlane(lo);
             bounds(a);
         } else {
             n = seg / a.per_seq;

@@ -157,7 +157,7 @@ def test_scan_without_what_is_optional(n, T, ch):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("lens", [[5], [1, 1, 1], [0, 3, 0, 0, 1, 40, 0], [100, 2, 17, 0, 300], [1] * 70, [64, 64, 128],
-                                  [700], [15, 0, 257, 1, 1, 60]])
+                                  [700], [15, 0, 257, 1, 1, 60], [3] * 150, [0] * 40 + [2] * 30 + [0, 90] + [0] * 70])
 def test_scan_packed(lens, dt):
     """Against each sequence's definition; behind the last sequence nothing changes; in place alike."""
     rng = np.random.default_rng(sum(lens))
