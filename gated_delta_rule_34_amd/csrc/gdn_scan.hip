@@ -624,14 +624,17 @@ __global__ __launch_bounds__(256) void scan_copy_kernel(const float *src, float 
 // sequences (128 groups of channels) 231 us in four parts, 302 in one; 5 (160)
 // 334 in four parts, which are more than two workgroups to a compute unit, and
 // 302 in one; 7 (224) 392 and 304.  Twice or half as many parts: 8192 tokens
-// of 2048 channels 128 and 142 us for 123.
+// of 2048 channels 128 and 142 us for 123.  A second launch and parts that
+// begin and end do not pay for few tokens: with 16 states 200 of them take 18 us
+// in one part and 21 in parts of 64, 300 25 and 21; with 64 states 150 take 35,
+// and 24 in parts of 32 (in parts of 64 36).
 ScanPlan scan_plan(int seqs, int T, int total, int ch, int N, bool packed) {
     const long groups = (ch + kCH - 1) / kCH;
     ScanPlan p{};
     const long base = packed ? groups : groups * seqs;
     const long len = packed ? total : T;
-    long k = base > 128 ? 1 : 512 / base;
-    const long most = (len + 63) / 64;
+    long k = base > 128 || len * (N + 16) <= 8192 ? 1 : 512 / base;
+    const long most = N >= 32 ? (len + 31) / 32 : (len + 63) / 64;
     if (k > most) k = most;
     long L = (len + k - 1) / k;
     L = (L + kTT - 1) / kTT * kTT;

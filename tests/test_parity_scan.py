@@ -125,7 +125,7 @@ def _check(y, h, ref, dt, what=""):
 
 # one token; part tiles; one segment (many groups of channels); a sequence in parts; odd channels; each state count
 SCAN = [(1, 1, 4, 8), (1, 3, 5, 16), (1, 100, 6, 8), (2, 40, 7, 16), (3, 1, 64, 16), (2, 5, 65, 32), (1, 16, 64, 64), (2, 17, 130, 16), (70, 40, 250, 8), (130, 20, 128, 16),
-        (1, 64, 64, 16), (1, 65, 64, 16), (1, 200, 70, 16), (2, 333, 129, 32), (1, 1000, 40, 8), (3, 150, 24, 64)]
+        (1, 64, 64, 16), (1, 65, 64, 16), (1, 200, 70, 16), (1, 256, 64, 16), (1, 257, 70, 16), (1, 103, 64, 64), (2, 333, 129, 32), (1, 1000, 40, 8), (3, 150, 24, 64)]
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
@@ -157,7 +157,7 @@ def test_scan_without_what_is_optional(n, T, ch):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("lens", [[5], [1, 1, 1], [0, 3, 0, 0, 1, 40, 0], [100, 2, 17, 0, 300], [1] * 70, [64, 64, 128],
-                                  [700], [15, 0, 257, 1, 1, 60], [3] * 150, [0] * 40 + [2] * 30 + [0, 90] + [0] * 70])
+                                  [700], [15, 0, 257, 1, 1, 60], [3] * 150, [64, 192, 10, 64],  [0] * 40 + [2] * 30 + [0, 90] + [0] * 70])
 def test_scan_packed(lens, dt):
     """Against each sequence's definition; behind the last sequence nothing changes; in place alike."""
     rng = np.random.default_rng(sum(lens))
