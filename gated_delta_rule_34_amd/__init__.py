@@ -812,7 +812,7 @@ def gdn_add_layernorm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=N
     if out is not None:
         _need(y, "out", shape, odt, dev)
     mean = torch.empty(shape[:-1], dtype=f32, device=dev) if return_stats else None
-    rstd = torch.empty(shape[:-1], dtype=f32, device=dev) if return_stats else None
+    rstd = torch.empty_like(mean) if return_stats else None
     y_scale = torch.empty(shape[:-1], dtype=f32, device=dev) if odt == torch.float8_e4m3fn else None
     _on_device(load().gdn_add_layernorm, "gdn_add_layernorm", dev,
                _addr(x), _addr(residual), _addr(weight), _addr(bias), _addr(y), _addr(r), _addr(mean), _addr(rstd),
@@ -843,8 +843,8 @@ def gdn_add_layernorm_bwd(dy, r, weight, mean, rstd, dr=None, need_dweight=True,
     if dr is not None:
         _need(dr, "dr", shape, r.dtype, dev)
     dx = torch.empty_like(r)
-    dw = torch.empty((D,), dtype=f32, device=dev) if need_dweight else None
-    db = torch.empty((D,), dtype=f32, device=dev) if need_dbias else None
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = torch.empty_like(weight) if need_dbias else None
     ws, nbytes = None, 0
     lib = load()
     if need_dweight or need_dbias:
@@ -1124,7 +1124,7 @@ def _conv(name, x, weight, cu, seqs, bias, act, conv_state, update_conv_state, o
             raise ValueError("update_conv_state needs conv_state")
         state = conv_state
     else:
-        state = torch.empty((seqs, W - 1, C), dtype=f32, device=dev)
+        state = torch.empty((seqs, W - 1, C), dtype=f32, device=dev) if conv_state is None else torch.empty_like(conv_state)
     y = torch.empty_like(x) if out is None else out
     if out is not None:
         _need(y, "out", lead + (C,), x.dtype, dev)
@@ -1199,8 +1199,11 @@ def _scan(name, x, dt, A, B, C, cu, seqs, D, z, dt_bias, h0, output_final_state,
         _need(y, "out", tuple(x.shape), x.dtype, dev)
     ht = None
     if output_final_state:
-        ht = torch.empty((seqs, ch, N), dtype=f32, device=dev) if final_state is None else final_state
-        _need(ht, "final_state", (seqs, ch, N), f32, dev)
+        if final_state is not None:
+            ht = final_state
+            _need(ht, "final_state", (seqs, ch, N), f32, dev)
+        else:
+            ht = torch.empty((seqs, ch, N), dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
     code = _code(x.dtype, "x")
     lib = load()
     T = x.shape[0] if cu is not None else x.shape[1]
@@ -1255,7 +1258,8 @@ def gdn_selective_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, out=
     ch, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
     _need(state, "state", (n, ch, N), torch.float32, dev)
     new = state if state_out is None else state_out
-    _need(new, "state_out", (n, ch, N), torch.float32, dev)
+    if state_out is not None:
+        _need(new, "state_out", (n, ch, N), torch.float32, dev)
     y = torch.empty_like(x) if out is None else out
     if out is not None:
         _need(y, "out", (n, ch), x.dtype, dev)
