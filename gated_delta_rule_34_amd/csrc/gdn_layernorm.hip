@@ -25,6 +25,22 @@
 
 namespace gdn {
 
+// A thread's eight columns.  In a row that is no multiple of eight the last ones
+// begin that much earlier, over columns that another thread has too: both
+// compute and store the same values there, with whole 16-byte accesses, and
+// `dup` of them are left out of this thread's sums (8: the row ends before this
+// piece, which only reads).  One by one, the last columns cost more than the rest
+// of the row: 32800 x 1023 in bf16 70 against 50 us, the backward 99 against 55;
+// 8194 x 4095 76 against 61 and 135 against 72 (rows that begin inside a
+// 16-byte word; 8200 x 4092 takes 52 and 59).
+struct Piece {
+    int c, dup;
+    __device__ __forceinline__ Piece(int c0, int D) : c(max(min(c0, D - 8), 0)), dup(min(c0 - c, 8)) {}
+    __device__ __forceinline__ bool live() const { return dup < 8; }
+    __device__ __forceinline__ bool whole(int D) const { return dup == 0 && c + 8 <= D; }
+    __device__ __forceinline__ bool counts(int e, int D) const { return e >= dup && c + e < D; }
+};
+
 // Two sums over the TPR threads of a row in one exchange; sh holds TPR / 64
 // pairs and is written once per call.
 template <int TPR>
@@ -57,39 +73,59 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
     const long row = (long)blockIdx.x * RPB + threadIdx.x / TPR;
     if (row >= rows) return;  // whole waves leave, and only where a row is one wave
     const XT *xr = x + row * D;
+    const auto piece = [&](int i) { return Piece((tid + i * TPR) * 8, D); };
     float u[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load_piece(u[i], xr, (tid + i * TPR) * 8, D);
+    for (int i = 0; i < NV; ++i) load_piece(u[i], xr, piece(i).c, D);
     if (res) {
         const RT *rr = res + row * D;
         float t[NV][8];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) load_piece(t[i], rr, (tid + i * TPR) * 8, D);
+        for (int i = 0; i < NV; ++i) load_piece(t[i], rr, piece(i).c, D);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[i][e] += t[i][e];
-        if (rout)  // may be res itself: this thread has read what it replaces
-#pragma unroll
-            for (int i = 0; i < NV; ++i) store_piece(rout + row * D, u[i], (tid + i * TPR) * 8, D);
     }
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const Piece p = piece(i);
+        if (p.whole(D)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += u[i][e];
+            for (int e = 0; e < 8; ++e) sum += u[i][e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += p.counts(e, D) ? u[i][e] : 0.f;
+        }
+    }
     // The mean's own rounding moves every difference alike: their sum says by
     // how much, and takes it out of the variance and of the differences.
     const float m = row_sum<TPR>(sum, sh[0]) / (float)D;
+    if (res && rout) {  // may be res itself: every thread of the row has read by now (each has added to the sum)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (piece(i).live()) store_piece(rout + row * D, u[i], piece(i).c, D);
+    }
     float ss = 0.f, sd = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int left = D - (tid + i * TPR) * 8;  // columns of this piece and after it
+        const Piece p = piece(i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            u[i][e] = e < left ? u[i][e] - m : 0.f;
-            ss = fmaf(u[i][e], u[i][e], ss);
-            sd += u[i][e];
+        for (int e = 0; e < 8; ++e) u[i][e] -= m;
+        if (p.whole(D)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(u[i][e], u[i][e], ss);
+                sd += u[i][e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = p.counts(e, D) ? u[i][e] : 0.f;
+                ss = fmaf(v, v, ss);
+                sd += v;
+            }
         }
     }
     const float2 both = row_sum2<TPR>(ss, sd, sh2);
@@ -103,8 +139,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         float wv[8], bv[8];
-        load_piece(wv, w, (tid + i * TPR) * 8, D);
-        if (b) load_piece(bv, b, (tid + i * TPR) * 8, D);
+        load_piece(wv, w, piece(i).c, D);
+        if (b) load_piece(bv, b, piece(i).c, D);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             u[i][e] = (u[i][e] - off) * s;
@@ -125,11 +161,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
         if (tid == 0) yscale[row] = scale;
         const QuantRow q(scale);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) store_piece_f8((uint8_t *)y + row * D, u[i], q, (tid + i * TPR) * 8, D);
+        for (int i = 0; i < NV; ++i)
+            if (piece(i).live()) store_piece_f8((uint8_t *)y + row * D, u[i], q, piece(i).c, D);
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) store_piece(y + row * D, u[i], (tid + i * TPR) * 8, D);
+        for (int i = 0; i < NV; ++i)
+            if (piece(i).live()) store_piece(y + row * D, u[i], piece(i).c, D);
     }
+}
+
+constexpr int ln_bwd_waves(int dy_bytes, int TPR, int NV) {
+    return NV == 2 && (dy_bytes == 2 || TPR == 64) ? 3 : 1;
 }
 
 // Backward.  A workgroup walks rows (its first row, then every RPB * grid rows
@@ -140,11 +182,16 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
 // (AHEAD).  32768 x 1024 in bf16 with dr 51 us, 5.2 TB/s of dy, r, dr and dx;
 // 16384 x 5120 in fp32 197 us, 5.1; beyond 8192 columns the two sums a column
 // crowd the registers: 4096 x 16384 in bf16 100 us, 4.0.
-template <class DT, class RT, int TPR, int NV>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT *dy, const RT *r, const float *w,
-                                                                       const float *mean, const float *rstd,
-                                                                       const RT *dr, RT *dx, float *part, long rows,
-                                                                       int D) {
+// Two pieces a thread are held to the registers of three waves a SIMD unit
+// where that spills little: 43690 x 768 with a fp32 residual 93 us against 131
+// at two waves, all in fp32 103 against 139; but 8192 x 4096 all in fp32, which
+// spills into its walk, 112 against 104, and keeps two.
+// ODD, a width that is no multiple of eight, leaves the columns that come twice
+// out of the sums; the others are spared its registers.
+template <class DT, class RT, int TPR, int NV, bool ODD>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR, ln_bwd_waves(sizeof(DT), TPR, NV)) void ln_bwd_kernel(
+    const DT *dy, const RT *r, const float *w, const float *mean, const float *rstd, const RT *dr, RT *dx, float *part,
+    long rows, int D) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     constexpr bool AHEAD = TPR < 1024 && !(NV == 4 && sizeof(RT) == 4);
     using DRaw = typename RawOf<DT>::type;
@@ -152,6 +199,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT 
     __shared__ float2 sh[2][TPR / 64 + 1];
     __shared__ float shw[RPB > 1 ? RPB * TPR * 8 : 1];
     const int tid = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const auto piece = [&](int i) { return Piece((tid + i * TPR) * 8, ODD ? D : 1 << 30); };
     f32x8 aw[NV], ab[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) aw[i] = ab[i] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -162,12 +210,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT 
         m0 = mean[row];
         s0 = rstd[row];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) g0[i] = load_raw(dy + row * D, (tid + i * TPR) * 8, D);
+        for (int i = 0; i < NV; ++i) g0[i] = load_raw(dy + row * D, piece(i).c, D);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r0[i] = load_raw(r + row * D, (tid + i * TPR) * 8, D);
+        for (int i = 0; i < NV; ++i) r0[i] = load_raw(r + row * D, piece(i).c, D);
         if (dr) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) d0[i] = load_raw(dr + row * D, (tid + i * TPR) * 8, D);
+            for (int i = 0; i < NV; ++i) d0[i] = load_raw(dr + row * D, piece(i).c, D);
         }
     };
     const long step = (long)gridDim.x * RPB;
@@ -181,8 +229,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT 
         float dot = 0.f, sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            // past the row's end dy and w are zero, so what xhat holds there does not count
-            const f32x8 wv = load8v(w, (tid + i * TPR) * 8, D);
+            const Piece p = piece(i);
+            const f32x8 wv = load8v(w, p.c, D);
             g[i] = raw_f32(g0[i]);
             xh[i] = raw_f32(r0[i]);
             d1[i] = d0[i];
@@ -192,8 +240,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT 
                 aw[i][e] = fmaf(g[i][e], xh[i][e], aw[i][e]);
                 ab[i][e] += g[i][e];
                 g[i][e] *= wv[e];
-                sum += g[i][e];
-                dot = fmaf(g[i][e], xh[i][e], dot);
+                if constexpr (!ODD) {  // past the row's end dy and w are zero
+                    sum += g[i][e];
+                    dot = fmaf(g[i][e], xh[i][e], dot);
+                }
+            }
+            if constexpr (!ODD) continue;
+            if (p.whole(D)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum += g[i][e];
+                    dot = fmaf(g[i][e], xh[i][e], dot);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = p.counts(e, D) ? g[i][e] : 0.f;
+                    sum += v;
+                    dot = p.counts(e, D) ? fmaf(v, xh[i][e], dot) : dot;
+                }
             }
         }
         if (AHEAD && row + step < rows) load(row + step);
@@ -212,7 +277,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] += d[e];
             }
-            store8v(dx + row * D, v, (tid + i * TPR) * 8, D);
+            if (piece(i).live()) store8v(dx + row * D, v, piece(i).c, D);
         }
     }
     if (!part) return;
@@ -235,12 +300,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_bwd_kernel(const DT 
 #pragma unroll
                         for (int p = 0; p < RPB; ++p) v[e] += shw[(p * 8 + e) * TPR + tid];
                     }
-                    store8v(pr + h * D, v, (tid + i * TPR) * 8, D);
+                    if (piece(i).live()) store8v(pr + h * D, v, piece(i).c, D);
                 }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) store8v(pr + h * D, acc[i], (tid + i * TPR) * 8, D);
+            for (int i = 0; i < NV; ++i)
+                if (piece(i).live()) store8v(pr + h * D, acc[i], piece(i).c, D);
         }
     }
 }
@@ -335,8 +401,9 @@ static hipError_t launch_ln_bwd_t(const void *dy, const void *r, const float *w,
     float *pp = dw || db ? part : nullptr;
 #define GDN_LNB(MOST, TPRv, NVv)                                                                                      \
     if (D <= MOST) {                                                                                                  \
-        hipLaunchKernelGGL((ln_bwd_kernel<DT, RT, TPRv, NVv>), dim3((unsigned)nb), dim3(TPRv < 256 ? 256 : TPRv), 0, \
-                           st, (const DT *)dy, (const RT *)r, w, mean, rstd, (const RT *)dr, (RT *)dx, pp, rows, D);  \
+        const auto k = D % 8 ? ln_bwd_kernel<DT, RT, TPRv, NVv, true> : ln_bwd_kernel<DT, RT, TPRv, NVv, false>;      \
+        hipLaunchKernelGGL(k, dim3((unsigned)nb), dim3(TPRv < 256 ? 256 : TPRv), 0, st, (const DT *)dy,               \
+                           (const RT *)r, w, mean, rstd, (const RT *)dr, (RT *)dx, pp, rows, D);                      \
     } else
     GDN_LNB(512, 64, 1)
     GDN_LNB(1024, 64, 2)
