@@ -231,6 +231,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, ln_bwd_waves(sizeof(DT), TPR
         for (int i = 0; i < NV; ++i) {
             const Piece p = piece(i);
             const f32x8 wv = load8v(w, p.c, D);
+            const float before = dot;
             g[i] = raw_f32(g0[i]);
             xh[i] = raw_f32(r0[i]);
             d1[i] = d0[i];
@@ -245,7 +246,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, ln_bwd_waves(sizeof(DT), TPR
                     dot = fmaf(g[i][e], xh[i][e], dot);
                 }
             }
-            if constexpr (!ODD) continue;
+            if constexpr (!ODD) {  // and xhat is -mean rstd there: beyond fp32 it gave NaN
+                dot = p.c < D ? dot : before;
+                continue;
+            }
             if (p.whole(D)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
