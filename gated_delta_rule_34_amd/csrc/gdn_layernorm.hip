@@ -113,6 +113,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void ln_kernel(const XT *x, 
         const Piece p = piece(i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[i][e] -= m;
+        if (F8 && D < 8) {
+            // what lies past such a row takes part in its largest magnitude: zero, as -mean rstd may be beyond fp32
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[i][e] = e < D ? u[i][e] : 0.f;
+        }
         if (p.whole(D)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {

@@ -40,3 +40,14 @@ def test_gradients_of_a_row_of_one_large_value(D, xd, rd):
     assert (np.abs(_h(dx) - rx) <= 2.0 ** -17 * mag + (2.0 ** -8 if rd == BF else 0) * np.abs(rx)).all()
     assert (np.abs(_h(dw) - rw) <= 2.0 ** -16 * (np.abs(_h(dy)) * xhat).sum(0)).all()
     assert (np.abs(_h(db) - rb) <= 2.0 ** -16 * np.abs(_h(dy)).sum(0)).all()
+
+
+@pytest.mark.parametrize("xd", [BF, F32])
+@pytest.mark.parametrize("D", [1, 2, 4, 8, 64])
+def test_8_bits_of_a_row_of_one_large_value(D, xd):
+    """The differences are zero, the mean times rstd is beyond fp32: codes of zero with scale 1."""
+    x = torch.full((5, D), 2.0 ** 60, dtype=xd, device="cuda")
+    q, _, mean, rstd, scale = gdn.gdn_add_layernorm(x, torch.ones(D, device="cuda"), eps=1e-44, out_dtype=F8,
+                                                    return_stats=True)
+    assert (mean == 2.0 ** 60).all() and not torch.isfinite(mean * rstd).any()
+    assert (q.float() == 0).all() and (scale == 1).all()
