@@ -1,0 +1,77 @@
+"""The selective scan against its fp64 definition where test_parity_scan.py
+does not look: small steps, and extreme ones in sequences of many parts.  The
+bars are those of test_parity_scan.py."""
+import numpy as np
+import pytest
+
+import gated_delta_rule_34_amd as gdn
+from oracle import scan as sc
+
+torch = pytest.importorskip("torch")
+
+BF, F32 = torch.bfloat16, torch.float32
+gpu = pytest.mark.gpu
+HALF = {BF: 2.0 ** -8, F32: 0.0}
+
+
+def _t(rng, shape, dt, scale=1.0):
+    return torch.from_numpy((scale * rng.standard_normal(shape)).astype(np.float32)).to(dt).cuda()
+
+
+def _h(t):
+    return None if t is None else t.detach().float().cpu().double().numpy()
+
+
+def _inputs(rng, lead, ch, N, dt, z=True, h0=0):
+    p = {"x": _t(rng, lead + (ch,), dt), "dt": _t(rng, lead + (ch,), dt), "B": _t(rng, lead + (N,), dt),
+         "C": _t(rng, lead + (N,), dt), "A": -torch.exp(_t(rng, (ch, N), F32)), "D": _t(rng, (ch,), F32),
+         "dt_bias": _t(rng, (ch,), F32) - 3.0, "z": _t(rng, lead + (ch,), dt, 2.0) if z else None}
+    p["h0"] = _t(rng, (h0, ch, N), F32) if h0 else None
+    return p
+
+
+def _check(y, h, p, T, dt, what=""):
+    keys = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "h0")
+    ry, rh, by, bh = sc.selective_scan(*(_h(p[k]) for k in keys), per_step=T * 2.0 ** -24)
+    for got, ref, bar, name in ((_h(y), ry, by + HALF[dt] * (np.abs(ry) + by), "y"), (_h(h), rh, bh, "h")):
+        bad = np.abs(got - ref) - bar
+        assert np.isfinite(got).all() and bad.max() <= 0, f"{what}{name}: worst excess {bad.max():.3e}"
+
+
+@gpu
+@pytest.mark.parametrize("N", [16, 64])
+def test_extreme_steps_and_decays_in_parts(N):
+    """softplus from far below zero to far above; decays that underflow; A of zero: through a sequence of many parts."""
+    rng = np.random.default_rng(4)
+    T = 600
+    assert gdn.gdn_selective_scan_workspace(1, T, 64, N) > 0
+    p = _inputs(rng, (1, T), 64, N, F32, h0=1)
+    p["dt"] = torch.linspace(-60, 60, T, device="cuda")[None, :, None].expand(1, T, 64).contiguous()
+    p["dt_bias"] = torch.zeros(64, device="cuda")
+    p["A"][:, 3] = 0.0
+    p["A"][:, 4] = -1e30
+    y, h = gdn.gdn_selective_scan(**p)
+    _check(y, h, p, T, F32)
+    p["dt"] = p["dt"].flip(1).contiguous()
+    y, h = gdn.gdn_selective_scan(**p)
+    _check(y, h, p, T, F32)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_small_steps_keep_their_relative_accuracy(dt):
+    """One token, x = B = 1 and no state before it: h is d = softplus(dt), within 2^-20 of itself down to where it
+    leaves fp32's normal range; and what the limits give."""
+    ch = 2048
+    v = torch.linspace(-86, 30, ch).to(dt)
+    v[-4:] = torch.tensor([float("inf"), -float("inf"), 3e38, -3e38]).to(dt)
+    one = lambda *shape, d=dt: torch.ones(shape, dtype=d, device="cuda")  # noqa: E731
+    A, h0 = -one(ch, 8, d=F32), torch.zeros(1, ch, 8, device="cuda")
+    _, h = gdn.gdn_selective_scan(one(1, 1, ch), v.cuda()[None, None], A, one(1, 1, 8), one(1, 1, 8))
+    _, s = gdn.gdn_selective_step(one(1, ch), v.cuda()[None], A, one(1, 8), one(1, 8), h0)
+    want = sc.softplus(v.double().numpy())[:-4]
+    for got in (h, s):
+        got = _h(got)[0]
+        assert (got == got[:, :1]).all()
+        assert (np.abs(got[:-4, 0] - want) <= 2.0 ** -20 * want).all()
+        assert got[-4, 0] == np.inf and got[-3, 0] == 0 and got[-2, 0] == float(v[-2]) and got[-1, 0] == 0
