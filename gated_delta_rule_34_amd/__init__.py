@@ -1159,12 +1159,15 @@ def gdn_causal_conv_varlen(x, weight, cu_seqlens, bias=None, act="silu", conv_st
                  update_conv_state, out)
 
 
+_SCAN_CHANNELS = 4  # the fewest that the scan's kernels take; fewer are filled up with channels of zeros
+
+
 def gdn_selective_scan_workspace(B, T, ch, N):
-    return int(load().gdn_selective_scan_workspace(B, T, ch, N))
+    return int(load().gdn_selective_scan_workspace(B, T, max(ch, _SCAN_CHANNELS) if ch > 0 else ch, N))
 
 
 def gdn_selective_scan_varlen_workspace(seqs, total_T, ch, N):
-    return int(load().gdn_selective_scan_varlen_workspace(seqs, total_T, ch, N))
+    return int(load().gdn_selective_scan_varlen_workspace(seqs, total_T, max(ch, _SCAN_CHANNELS) if ch > 0 else ch, N))
 
 
 def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
@@ -1188,6 +1191,13 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
     return ch, N
 
 
+def _overlap(a, b):
+    if b is None:
+        return False
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    return a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size()
+
+
 def _scan(name, x, dt, A, B, C, cu, seqs, D, z, dt_bias, h0, output_final_state, workspace, out, final_state):
     torch = _torch()
     dev, f32 = x.device, torch.float32
@@ -1204,6 +1214,28 @@ def _scan(name, x, dt, A, B, C, cu, seqs, D, z, dt_bias, h0, output_final_state,
             _need(ht, "final_state", (seqs, ch, N), f32, dev)
         else:
             ht = torch.empty((seqs, ch, N), dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
+    if 0 < ch < _SCAN_CHANNELS:
+        # what the call below would refuse of the given buffers, and no longer sees
+        read = [x, dt, A, B, C, cu, D, z, dt_bias]
+        bad = any(_overlap(y, t) for t in read + [h0, ht])
+        if ht is not None:
+            in_place = h0 is not None and h0.data_ptr() == ht.data_ptr()
+            bad = bad or any(_overlap(ht, t) for t in read + ([] if in_place else [h0]))
+        _check(int(bad), name)
+
+        def last(t):
+            return None if t is None else torch.nn.functional.pad(t, (0, _SCAN_CHANNELS - ch))
+
+        def rows(t):
+            return None if t is None else torch.nn.functional.pad(t, (0, 0, 0, _SCAN_CHANNELS - ch))
+
+        # a given out keeps what it holds for tokens of no sequence
+        wide, state = _scan(name, last(x), last(dt), rows(A), B, C, cu, seqs, last(D), last(z), last(dt_bias), rows(h0),
+                            output_final_state, workspace, last(out), None)
+        y.copy_(wide[..., :ch])
+        if ht is not None:
+            ht.copy_(state[:, :ch])
+        return y, ht
     code = _code(x.dtype, "x")
     lib = load()
     T = x.shape[0] if cu is not None else x.shape[1]
@@ -1230,8 +1262,8 @@ def gdn_selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, ou
                        out=None, final_state=None):
     """Selective state space scan: d = softplus(dt + dt_bias), h_t = exp(d A) h_{t-1} + d x B, y = (C . h + D x) silu(z).
     x, dt, z [batch,T,ch] and B, C [batch,T,N] in one type (bf16 or fp32); A [ch,N], D, dt_bias [ch] fp32 (z, D and
-    dt_bias may be None); h0 [batch,ch,N] fp32 or None; N 8, 16, 32 or 64.  final_state may be h0 itself.  Returns (y in
-    the type of x, final state or None)."""
+    dt_bias may be None); h0 [batch,ch,N] fp32 or None; N 8, 16, 32 or 64.  final_state may be h0 itself.  One to three
+    channels are scanned as four, in copies filled up with zeros.  Returns (y in the type of x, final state or None)."""
     if x.dim() != 3:
         raise ValueError(f"x must be [batch, T, channels], got {tuple(x.shape)}")
     return _scan("gdn_selective_scan", x, dt, A, B, C, None, x.shape[0], D, z, dt_bias, h0, output_final_state, workspace,

@@ -646,8 +646,9 @@ gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bi
  * channels are cut along their tokens (a fixed cut for the sizes); the state
  * then enters a part as the part before it left it, in fp32.
  *   ws  gdn_selective_scan_workspace() bytes, 256-byte aligned (may be NULL if 0)
- * ch any value from 4 to 2^24; at most 2^30 tokens.  x, dt, Bm, Cm, z, y, A, h0 and ht 16-byte
- * aligned, D and dt_bias 4-byte.
+ * ch any value from 4 to 2^24 (a caller with fewer adds channels of zeros, which
+ * the Python binding does by itself); at most 2^30 tokens.  x, dt, Bm, Cm, z, y,
+ * A, h0 and ht 16-byte aligned, D and dt_bias 4-byte.
  * gdn_selective_scan_varlen: the same on `seqs` packed sequences (x, dt, z, y
  * [total_T, ch], Bm, Cm [total_T, N], states [seqs, ch, N]); cu_seqlens as in
  * gdn_chunk_fwd_varlen (an empty sequence passes its state on; tokens that

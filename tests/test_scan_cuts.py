@@ -1,6 +1,6 @@
 """The selective scan against its fp64 definition where test_parity_scan.py
-does not look: small steps, and extreme ones in sequences of many parts.  The
-bars are those of test_parity_scan.py."""
+does not look: small steps, extreme ones in sequences of many parts, and one to
+three channels.  The bars are those of test_parity_scan.py."""
 import numpy as np
 import pytest
 
@@ -75,3 +75,66 @@ def test_small_steps_keep_their_relative_accuracy(dt):
         assert (got == got[:, :1]).all()
         assert (np.abs(got[:-4, 0] - want) <= 2.0 ** -20 * want).all()
         assert got[-4, 0] == np.inf and got[-3, 0] == 0 and got[-2, 0] == float(v[-2]) and got[-1, 0] == 0
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("N", [8, 64])
+@pytest.mark.parametrize("n,T,ch", [(2, 40, 1), (3, 700, 2), (1, 1, 3), (5, 333, 3)])
+def test_few_channels(n, T, ch, N, dt):
+    """One to three channels, dense and packed, with and without what is optional, and the step that goes on from them."""
+    rng = np.random.default_rng(n + T + N)
+    p = _inputs(rng, (n, T), ch, N, dt, h0=n)
+    y, h = gdn.gdn_selective_scan(**p)
+    assert y.shape == (n, T, ch) and h.shape == (n, ch, N) and y.is_contiguous() and h.is_contiguous()
+    _check(y, h, p, T, dt)
+    held, out = dict(p, h0=p["h0"].clone()), torch.empty_like(y)
+    ws = torch.empty(gdn.gdn_selective_scan_workspace(n, T, ch, N) + 256, dtype=torch.uint8, device="cuda")
+    y2, h2 = gdn.gdn_selective_scan(**held, final_state=held["h0"], out=out, workspace=ws)
+    assert y2 is out and h2 is held["h0"] and torch.equal(y2, y) and torch.equal(h2, h)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda") * T
+    flat = {k: v.reshape(n * T, -1) if k in ("x", "dt", "B", "C", "z") else v for k, v in p.items()}
+    y3, h3 = gdn.gdn_selective_scan_varlen(**flat, cu_seqlens=cu)
+    _check(y3.view(n, T, ch), h3, p, T, dt)
+    tail = torch.full((n * T + 2, ch), 7.0, dtype=dt, device="cuda")
+    more = {k: torch.cat([v, v[:1], v[:1]]) if k in ("x", "dt", "B", "C", "z") else v for k, v in flat.items()}
+    y4, _ = gdn.gdn_selective_scan_varlen(**more, cu_seqlens=cu, out=tail)
+    assert y4 is tail and (tail[n * T:] == 7).all()
+    q = dict(p, D=None, z=None, dt_bias=None, h0=None, dt=p["dt"] - 3)
+    y5, h5 = gdn.gdn_selective_scan(**q)
+    _check(y5, h5, q, T, dt)
+    y6, none = gdn.gdn_selective_scan(**q, output_final_state=False)
+    assert none is None and torch.equal(y6, y5)
+    last = {k: p[k][:, -1].contiguous() for k in ("x", "dt", "B", "C", "z")}
+    ys, hs = gdn.gdn_selective_step(**last, A=p["A"], D=p["D"], dt_bias=p["dt_bias"], state=h.clone())
+    go = dict(p, h0=h, **{k: v[:, None].contiguous() for k, v in last.items()})
+    _check(ys[:, None], hs, go, 1, dt)
+    yg, hg = gdn.gdn_selective_scan(**go)
+    _check(yg, hg, go, 1, dt)
+    with pytest.raises(RuntimeError):
+        gdn.gdn_selective_scan(**p, out=p["x"])
+    with pytest.raises(RuntimeError):
+        gdn.gdn_selective_scan(**p, out=p["z"])
+    if dt == F32 and T >= N:        # out over what becomes the state
+        with pytest.raises(RuntimeError):
+            gdn.gdn_selective_scan(**p, out=y, final_state=y.view(-1)[:n * ch * N].view(n, ch, N))
+
+
+@gpu
+def test_few_channels_captured():
+    rng = np.random.default_rng(3)
+    p = _inputs(rng, (1, 300), 3, 16, BF, h0=1)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        gdn.gdn_selective_scan(**p)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = gdn.gdn_selective_scan(**p)
+    for _ in range(3):
+        p["x"].copy_(_t(rng, (1, 300, 3), BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        ey, eh = gdn.gdn_selective_scan(**p)
+        assert torch.equal(y, ey) and torch.equal(h, eh)
+        torch.cuda.synchronize()
