@@ -1,6 +1,13 @@
-"""The selective scan against its fp64 definition where test_parity_scan.py
-does not look: small steps, extreme ones in sequences of many parts, and one to
-three channels.  The bars are those of test_parity_scan.py."""
+"""Every form of the scan's kernel -- states, scanning waves, dense and packed,
+in one part and cut along the tokens -- against the fp64 definition; special
+values that pass from part to part; the accuracy of small steps; and states of
+one to three channels.
+
+The bars are those of test_parity_scan.py.  CPU tests hold the lists of sizes to
+what they are there for: the workspace says whether a call is cut, and into how
+many parts at least."""
+import os
+
 import numpy as np
 import pytest
 
@@ -11,7 +18,50 @@ torch = pytest.importorskip("torch")
 
 BF, F32 = torch.bfloat16, torch.float32
 gpu = pytest.mark.gpu
+built = pytest.mark.skipif(not os.path.exists(gdn.lib_path), reason="libgdn.so not built")
 HALF = {BF: 2.0 ** -8, F32: 0.0}
+STATES = [8, 16, 32, 64]
+CARD = 256  # workgroups, up to which 32 and 64 states take eight scanning waves
+
+# (sequences, tokens, channels): one part, few workgroups; one part, more than 256; in parts, few; in parts, more than
+# 256 (from 32 states on); in parts that end with the sequence (of 64 tokens, from 32 states on of 32)
+DENSE = [(2, 40, 72), (130, 20, 130), (3, 700, 70), (1, 1100, 520), (1, 512, 64), (2, 384, 64)]
+# sequences' lengths, and tokens behind the last one, channels
+PACKED = [([0, 3, 0, 0, 1, 40, 0], 5, 72), ([100, 2, 17, 0, 300, 64, 256], 3, 70), ([700, 1, 0, 399], 2, 520),
+          ([3] * 150, 1, 24), ([5, 0, 6], 0, 16500)]
+
+
+def _up(n):
+    return (n + 255) // 256 * 256
+
+
+def _parts(nbytes, seqs, ch, N):
+    """Parts of all sequences together, from what is kept between them: (N + 1) numbers a part and channel, N a
+    sequence and channel, in three pieces of whole 256 bytes."""
+    return (nbytes - _up(seqs * ch * N * 4)) // (ch * (N + 1) * 4) if nbytes else 0
+
+
+def _groups(ch):
+    return (ch + 63) // 64
+
+
+@built
+@pytest.mark.parametrize("N", STATES)
+def test_the_sizes_reach_every_form(N):
+    seen = set()
+    for n, T, ch in DENSE:
+        parts = _parts(gdn.gdn_selective_scan_workspace(n, T, ch, N), n, ch, N)
+        seen.add((parts > 0, (parts or n) * _groups(ch) > CARD))
+    every = {(False, False), (False, True), (True, False)} | ({(True, True)} if N >= 32 else set())
+    assert seen == every
+    step = 64 if N < 32 else 32
+    for n, T, ch in DENSE[-2:]:
+        assert T % step == 0 and _parts(gdn.gdn_selective_scan_workspace(n, T, ch, N), n, ch, N) == n * T // step
+    seen = set()
+    for lens, extra, ch in PACKED:
+        parts = _parts(gdn.gdn_selective_scan_varlen_workspace(len(lens), sum(lens) + extra, ch, N), len(lens), ch, N)
+        seen.add((parts > 0, (parts or 1) * _groups(ch) > CARD))
+    assert seen == every
 
 
 def _t(rng, shape, dt, scale=1.0):
@@ -39,6 +89,50 @@ def _check(y, h, p, T, dt, what=""):
 
 
 @gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("n,T,ch", DENSE)
+def test_dense(n, T, ch, N, dt):
+    rng = np.random.default_rng(n + T + N)
+    p = _inputs(rng, (n, T), ch, N, dt, h0=n)
+    y, h = gdn.gdn_selective_scan(**p)
+    _check(y, h, p, T, dt)
+    again = gdn.gdn_selective_scan(**p)
+    assert torch.equal(again[0], y) and torch.equal(again[1], h)
+    held = dict(p, h0=p["h0"].clone())
+    y2, h2 = gdn.gdn_selective_scan(**held, final_state=held["h0"])
+    assert h2 is held["h0"] and torch.equal(h2, h) and torch.equal(y2, y)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("N", STATES)
+@pytest.mark.parametrize("lens,extra,ch", PACKED)
+def test_packed(lens, extra, ch, N, dt):
+    rng = np.random.default_rng(sum(lens) + N)
+    T, k = sum(lens), len(lens)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    for h0 in (0, k):
+        p = _inputs(rng, (T + extra,), ch, N, dt, z=h0 > 0, h0=h0)
+        out = torch.full_like(p["x"], 7.0)
+        y, h = gdn.gdn_selective_scan_varlen(**p, cu_seqlens=cu, out=out)
+        assert (y[T:] == 7).all()
+        at = 0
+        for i, n in enumerate(lens):
+            if n == 0:
+                assert (h[i] == (p["h0"][i] if h0 else 0)).all()
+                continue
+            q = dict(p, **{s: p[s][None, at:at + n] for s in ("x", "dt", "B", "C") + (("z",) if h0 else ())})
+            q["h0"] = p["h0"][i:i + 1] if h0 else None
+            _check(y[None, at:at + n], h[i:i + 1], q, n, dt, f"sequence {i} ")
+            at += n
+        if h0:
+            held = dict(p, h0=p["h0"].clone())
+            y2, h2 = gdn.gdn_selective_scan_varlen(**held, cu_seqlens=cu, final_state=held["h0"])
+            assert torch.equal(h2, h) and torch.equal(y2[:T], y[:T])
+
+
+@gpu
 @pytest.mark.parametrize("N", [16, 64])
 def test_extreme_steps_and_decays_in_parts(N):
     """softplus from far below zero to far above; decays that underflow; A of zero: through a sequence of many parts."""
@@ -55,6 +149,27 @@ def test_extreme_steps_and_decays_in_parts(N):
     p["dt"] = p["dt"].flip(1).contiguous()
     y, h = gdn.gdn_selective_scan(**p)
     _check(y, h, p, T, F32)
+
+
+@gpu
+@pytest.mark.parametrize("N", [16, 64])
+@pytest.mark.parametrize("where", ["x", "dt"])
+def test_nan_stays_in_its_channel_and_sequence_in_parts(where, N):
+    rng = np.random.default_rng(5)
+    p = _inputs(rng, (2, 600), 130, N, F32)
+    assert gdn.gdn_selective_scan_workspace(2, 600, 130, N) > 0
+    want, hw = gdn.gdn_selective_scan(**p)
+    p[where][1, 40, 70] = float("nan")
+    y, h = gdn.gdn_selective_scan(**p)
+    assert torch.isnan(y[1, 40:, 70]).all() and torch.isnan(h[1, 70]).all()
+    y[1, 40:, 70], h[1, 70] = want[1, 40:, 70], hw[1, 70]
+    assert torch.equal(y, want) and torch.equal(h, hw)
+    cu = torch.tensor([0, 600, 1200], dtype=torch.int32, device="cuda")
+    flat = {k: v.reshape(1200, -1) if k in ("x", "dt", "B", "C", "z") else v for k, v in p.items()}
+    y, h = gdn.gdn_selective_scan_varlen(**flat, cu_seqlens=cu)
+    assert torch.isnan(y[640:, 70]).all() and torch.isnan(h[1, 70]).all()
+    y[640:, 70], h[1, 70] = 0, 0
+    assert torch.isfinite(y).all() and torch.isfinite(h).all()
 
 
 @gpu
