@@ -1,6 +1,7 @@
 // gdn_api.hip -- the C ABI declared in include/gdn.h: argument validation,
 // workspace layout and kernel sequencing on the caller's stream.  No device
 // memory is allocated here; every buffer belongs to the caller.
+#include <limits.h>
 #include <stdint.h>
 
 #include "../../include/gdn.h"
@@ -909,7 +910,8 @@ static gdn_status conv_call(const void *x, const float *w, const float *bias, co
     if (!x || !w || !y || seqs < 1 || T < 1 || C < 1) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(dtype) || W < 2 || W > 4 || (act != GDN_ACT_NONE && act != GDN_ACT_SILU)) return GDN_ERR_UNSUPPORTED;
     const long long octets = ((long long)C + 7) / 8;
-    if (total > (1 << 30) || total * octets >= (1LL << 32) - 256 || seqs * octets >= (1LL << 32) - 256)
+    // the kernels count channels past the last octet's end in 32 bits
+    if (C > INT_MAX - 16 || total > (1 << 30) || total * octets >= (1LL << 32) - 256 || seqs * octets >= (1LL << 32) - 256)
         return GDN_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w, 4) || !aligned(bias, 4) || !aligned(cu, 4) ||
         !aligned(state_in, 4) || !aligned(state_out, 4))

@@ -614,8 +614,8 @@ gdn_status gdn_gated_linear_bwd(const void *dy, const void *x, const void *w, co
  *   state_out  same layout, nullable: the W-1 inputs that end at the last
  *              token; may be state_in itself (updated in place)
  *   act    GDN_ACT_NONE or GDN_ACT_SILU
- * T = 1 with a state is one decode token.  C any value; B * T * C / 8 below
- * 2^32.  x and y 16-byte aligned, the others 4-byte.
+ * T = 1 with a state is one decode token.  C any value up to 2^31 - 17; B * T
+ * * C / 8 below 2^32.  x and y 16-byte aligned, the others 4-byte.
  * gdn_causal_conv_varlen: the same on N packed sequences, x, y [total_T, C] and
  * states [N, W-1, C]; cu_seqlens as in gdn_chunk_fwd_varlen (an empty sequence
  * passes its state on; tokens that belong to no sequence are left alone).
