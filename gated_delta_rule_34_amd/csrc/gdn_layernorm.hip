@@ -17,7 +17,9 @@
 // Rows are laid over threads as in the RMS norm: one wave up to 2048 columns
 // in the forward and 1024 in the backward, beyond that 256, 512 or 1024
 // threads with one LDS exchange per sum; columns in pieces of eight per
-// thread at element alignment.
+// thread at element alignment.  A row of fewer than 512 columns leaves lanes of
+// its wave idle: 131072 x 256 in bf16 with a residual 70 us, its backward with dr
+// 117, for 52 of bytes; 262144 x 128 117 and 205, 524288 x 64 215 and 389.
 #include "gdn_device.h"
 #include "gdn_launch.h"
 #include "gdn_row.h"
@@ -186,7 +188,9 @@ constexpr int ln_bwd_waves(int dy_bytes, int TPR, int NV) {
 // loads are issued before this row's sums where the registers hold both
 // (AHEAD).  32768 x 1024 in bf16 with dr 51 us, 5.2 TB/s of dy, r, dr and dx;
 // 16384 x 5120 in fp32 197 us, 5.1; beyond 8192 columns the two sums a column
-// crowd the registers: 4096 x 16384 in bf16 100 us, 4.0.
+// crowd the registers: 4096 x 16384 in bf16 100 us, 4.0; beyond 16384 they do
+// not fit, and 145 to 337 registers are spilled: 2048 x 32768 in bf16 with dr
+// 318 us, 1.7, with fp32 rows 473, 2.0.
 // Two pieces a thread are held to the registers of three waves a SIMD unit
 // where that spills little: 43690 x 768 with a fp32 residual 93 us against 131
 // at two waves, all in fp32 103 against 139; but 8192 x 4096 all in fp32, which
@@ -395,7 +399,9 @@ hipError_t launch_add_layernorm(const void *x, const void *res, const float *w, 
 // best (30 us, 768 32, 512 42), 32768 x 1024 768 (51 us, 384 58, 1024 62),
 // 16384 x 5120 in fp32 512 (197 us, 256 244, 768 228), 4096 x 4096 in bf16 512
 // (33 us, 1024 42), 4096 x 8192 256 (45 us, 128 62, 512 53), 4096 x 16384 256
-// (100 us, 512 112).
+// (100 us, 512 112).  Not swept below 4096 rows, where a workgroup has a few
+// rows and the partial sums weigh: 3294 x 1080 takes 14.7 + 4.1 us for 4.2 of
+// the rows' bytes, 13 MB of sums beside 21 MB.
 int ln_bwd_blocks(long rows, int D) {
     const long groups = D <= 1024 ? (rows + 3) / 4 : rows;
     const long most = D <= 512 ? 1024 : D <= 2048 ? 768 : D <= 6144 ? 512 : 256;

@@ -388,14 +388,21 @@ struct Walk {
 // the parts of y into outputs a tile behind.  One barrier a tile.
 // Bound by the vector unit: a state costs a token four instructions and an
 // exponential (4.2 and 8.4 clocks each, measured), the rest of a channel and
-// token 125 / 16 instructions and one exponential and one reciprocal, twice.
-// 8 x 4096 x 2048 channels, 16 states, bf16 with skip and gate: that is 250 us,
-// and takes 302 with 256 workgroups, whose two waves a SIMD leave gaps (vector
-// unit busy 85 %; a single wave issues one instruction in 5.6 clocks), 255 with
-// two workgroups to a compute unit (16 x 2048 tokens).  HBM would take 105 us.
-// Tried and not kept: the 4x4x1 matrix products for B (d x) and for y (362 us;
-// for the first alone 310, and 250 with two workgroups), decays computed a
-// group of tokens ahead (310), staging two tiles ahead (313).
+// token 37 instructions, two exponentials and two reciprocals (counted).
+// 8 x 4096 x 2048 channels, 16 states, bf16 with skip and gate: that is 253 us
+// at 2.4 GHz, and takes 306 with 256 workgroups, whose two waves a SIMD leave
+// gaps (vector unit busy 76 %; a single wave issues one instruction in 5.6
+// clocks), 260 with two workgroups to a compute unit (16 x 2048 tokens).  HBM
+// would take 105 us.  With 8 states the rest weighs as much as the states: 8 x
+// 4096 x 2048 245 us for 166 of instructions.
+// Tried and not kept, for 302 us then: the 4x4x1 matrix products for B (d x)
+// and for y (362 us; for the first alone 310, and 250 with two workgroups),
+// decays computed a group of tokens ahead (310), staging two tiles ahead (313).
+// A tile never crosses a sequence's end and a sequence's entry state is asked
+// for when its first tile comes: 2000 sequences of 4 tokens of 2048 channels
+// 276 us, 256 of one token beside one of 2000 154 (that one alone takes 42, 256
+// steps 15).  Sequences without tokens are walked one by one, about 0.2 us each:
+// 4000 of them around one of 300 tokens of 256 channels 790 us for 16.
 // CARRY: only the state at the segment's end, and the sum of d, for the
 // segments that follow (E, F); with several segments a sequence's state enters
 // a segment as E of the last, plus exp(A F) times what entered that, and so on
@@ -640,7 +647,8 @@ __global__ __launch_bounds__(256) void scan_copy_kernel(const float *src, float 
 // of 2048 channels 128 and 142 us for 123.  A second launch and parts that
 // begin and end do not pay for few tokens: with 16 states 200 of them take 18 us
 // in one part and 21 in parts of 64, 300 25 and 21; with 64 states 150 take 35,
-// and 24 in parts of 32 (in parts of 64 36).
+// and 24 in parts of 32 (in parts of 64 36).  64 states, of which a compute unit
+// holds one workgroup, are cut for two like the others.
 ScanPlan scan_plan(int seqs, int T, int total, int ch, int N, bool packed) {
     const long groups = (ch + kCH - 1) / kCH;
     ScanPlan p{};
@@ -673,11 +681,15 @@ static hipError_t scan_run(const ScanArgs &a, const ScanPlan &p, hipStream_t st)
         if (e != hipSuccess) return e;
     }
     if constexpr (N >= 32) {
-        // one workgroup to a compute unit: eight scanning waves, so that each
-        // SIMD has three waves to choose from (8 x 2048 x 2048 channels with 32
-        // states 236 us against 269 with four, 8 x 1024 x 2048 with 64 205
-        // against 230; with 16, two to a lane, the reads from LDS outweigh it:
-        // 8 x 4096 x 2048 358 against 302)
+        // at most one workgroup to each compute unit: eight scanning waves, so
+        // that each SIMD has three waves to choose from (8 x 2048 x 2048
+        // channels with 32 states 237 us against 269 with four, 8 x 1024 x 2048
+        // with 64 205 against 230; with 16, two to a lane, the reads from LDS
+        // outweigh it: 8 x 4096 x 2048 358 against 302).  More workgroups take
+        // four, two of which share a compute unit with 32 states.  With 64 the
+        // four-wave form takes 140 registers, three waves a SIMD, and so runs
+        // alone, too; eight waves would serve there as well: 16 x 1024 x 2048
+        // 457 us so and 408 with eight, 1 x 8192 x 2048 in parts 398 and 375.
         if (grid.x <= 256) {
             if (a.cu) hipLaunchKernelGGL((scan_kernel<ET, N, 8, true, false>), grid, dim3(768), 0, st, a);
             else hipLaunchKernelGGL((scan_kernel<ET, N, 8, false, false>), grid, dim3(768), 0, st, a);

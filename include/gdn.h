@@ -444,7 +444,8 @@ gdn_status gdn_quantize_rows(const void *x, void *q, float *scale, long long row
  *   bias   [D] fp32, nullable
  *   mean, rstd  [rows] fp32, nullable: m and s, for gdn_add_layernorm_bwd
  *   the others as gdn_add_rmsnorm
- * Sizes, types, alignment, special values and errors as gdn_add_rmsnorm.
+ * Sizes, types, alignment, special values and errors as gdn_add_rmsnorm; here
+ * the sums of u and of (u - m)^2 must not overflow fp32.
  */
 gdn_status gdn_add_layernorm(const void *x, const void *residual, const float *weight, const float *bias, void *y,
                              void *r, float *mean, float *rstd, float *y_scale, long long rows, int D,
@@ -642,9 +643,10 @@ gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bi
  *   h0           [B, ch, N] fp32, nullable (zeros)
  *   ht           same, nullable: the state after the last token; may alias h0
  *                exactly
- * fp32 arithmetic and states, one rounding per output.  Few sequences of few
- * channels are cut along their tokens (a fixed cut for the sizes); the state
- * then enters a part as the part before it left it, in fp32.
+ * fp32 arithmetic and states (d within 2^-20 of itself), one rounding per
+ * output.  Few sequences of few channels are cut along their tokens (a fixed cut
+ * for the sizes); the state then enters a part as the part before it left it, in
+ * fp32.
  *   ws  gdn_selective_scan_workspace() bytes, 256-byte aligned (may be NULL if 0)
  * ch any value from 4 to 2^24 (a caller with fewer adds channels of zeros, which
  * the Python binding does by itself); at most 2^30 tokens.  x, dt, Bm, Cm, z, y,
