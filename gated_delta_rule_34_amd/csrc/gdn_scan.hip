@@ -29,7 +29,7 @@ __device__ __forceinline__ float silu_of(float z) {
 // of the rounding of ln 2 (8 x 4096 x 2048 channels with 16 states take 306 us
 // for 302 without).
 __device__ __forceinline__ float softplus(float v) {
-    const float a = fminf(fabsf(v), 160.f);  // finite for the correction; e is zero from 104 on
+    const float a = fminf(fabsf(v), 160.f);  // finite for the correction; e is zero there
     const float m = a * -LOG2E;
     float e = __builtin_amdgcn_exp2f(m);
     e = fmaf(e, fmaf(m, -0.693147182f, -a), e);

@@ -643,8 +643,8 @@ gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bi
  *   h0           [B, ch, N] fp32, nullable (zeros)
  *   ht           same, nullable: the state after the last token; may alias h0
  *                exactly
- * fp32 arithmetic and states (d within 2^-20 of itself), one rounding per
- * output.  Few sequences of few channels are cut along their tokens (a fixed cut
+ * fp32 arithmetic and states (d within 2^-20 of itself, as far as it is a normal
+ * fp32 number), one rounding per output.  Few sequences of few channels are cut along their tokens (a fixed cut
  * for the sizes); the state then enters a part as the part before it left it, in
  * fp32.
  *   ws  gdn_selective_scan_workspace() bytes, 256-byte aligned (may be NULL if 0)
