@@ -644,9 +644,9 @@ gdn_status gdn_causal_conv_varlen(const void *x, const float *w, const float *bi
  *   ht           same, nullable: the state after the last token; may alias h0
  *                exactly
  * fp32 arithmetic and states (d within 2^-20 of itself, as far as it is a normal
- * fp32 number), one rounding per output.  Few sequences of few channels are cut along their tokens (a fixed cut
- * for the sizes); the state then enters a part as the part before it left it, in
- * fp32.
+ * fp32 number), one rounding per output.  Few sequences of few channels are cut
+ * along their tokens (a fixed cut for the sizes); the state then enters a part as
+ * the part before it left it, in fp32.
  *   ws  gdn_selective_scan_workspace() bytes, 256-byte aligned (may be NULL if 0)
  * ch any value from 4 to 2^24 (a caller with fewer adds channels of zeros, which
  * the Python binding does by itself); at most 2^30 tokens.  x, dt, Bm, Cm, z, y,
